@@ -45,6 +45,10 @@ LORA_ERR_TIMEOUT = 8
 LORA_ERR_WORKSPACE = 9
 LORA_ERR_BOUNDS = 10
 
+LORA_KV_BF16 = 0
+LORA_KV_E4M3 = 1
+LORA_KV_INT8 = 2
+
 
 class lora_target(ctypes.Structure):
     _fields_ = [("d_in", _I), ("d_out", _I)]
@@ -98,6 +102,15 @@ _sig("lora_moe_workspace_bytes", _Z, [_P, _I, _I])
 _sig("lora_shrink", _I, [_P, _I, _P, _I, _P, _I, _P, _I, _P, _Z, _P])
 _sig("lora_expand", _I, [_P, _I, _P, _I, _P, _I, _P, _P, _I, _P, _Z, _P])
 _sig("lora_apply_noalloc", _I, [_P, _I, _P, _I, _P, _I, _P, _P, _I, _P])
+_sig("lora_kv_bytes_required", _Z, [_I, _I, _I, _I, _I, _I])
+_sig("lora_kv_create", _I, [ctypes.POINTER(_P), _I, _I, _I, _I, _I, _I, _I, _P, _Z])
+_sig("lora_kv_destroy", _I, [_P])
+_sig("lora_kv_get_error", _I, [_P, ctypes.POINTER(_I), _P])
+_sig("lora_kv_append", _I, [_P, _I, _P, _I, _P, _I, _P, _I, _P, _P, _I, _I, _P])
+_sig("lora_kv_gather", _I, [_P, _I, _P, _I, _P, _I, _P, _I, _P, _P, _I, _I, _P])
+_sig("lora_attend_workspace_bytes", _Z, [_P, _I])
+_sig("lora_attend", _I, [_P, _I, _P, _I, _P, _I, _P, _P, _I, _P, _I, _P, _I, ctypes.c_float, _I, _P, _Z, _P])
+_sig("lora_rmsnorm", _I, [_I, _P, _I, _P, _I, _P, _I, _P, ctypes.c_float, _P, _I, _P, _I, _P, _I, _I, _I, _P])
 _sig("lora_get_error", _I, [_P, ctypes.POINTER(_I), _P])
 _sig("lora_kernel_launches", ctypes.c_uint64, [])
 _sig("lora_set_wait_limit_ns", None, [ctypes.c_uint64])
@@ -352,6 +365,158 @@ def lora_apply_noalloc(pool: PoolHandle, target: int, x, y, ids, scales, stream=
     Calls that overlap on the GPU share that array and must be serialised."""
     _check(_lib.lora_apply_noalloc(pool, target, _ptr(x), _ld(x), _ptr(y), _ld(y), _ptr(ids), _ptr(scales),
                                    y.shape[0], _stream(stream)), "lora_apply_noalloc")
+
+
+# ---------------------------------------------------------------- the key/value cache
+
+
+class KvHandle:
+    """The opaque cache pointer plus the Python objects it must outlive."""
+
+    def __init__(self, ptr: int, device: int, mem, n_layers: int, n_pages: int, page_tokens: int, n_kv_heads: int,
+                 head_dim: int, kv_type: int):
+        self.ptr = ptr
+        self.device = device
+        self.mem = mem
+        self.n_layers, self.n_pages, self.page_tokens = n_layers, n_pages, page_tokens
+        self.n_kv_heads, self.head_dim, self.kv_type = n_kv_heads, head_dim, kv_type
+
+    @property
+    def _as_parameter_(self):
+        return self.ptr
+
+
+def _rows(t, name: str, device: int, width: int, dtype, where: str):
+    """A [T, ld] operand of a call that reads or writes T rows of `width` values through its row stride."""
+    if t.dtype != dtype or t.get_device() != device or t.dim() != 2 or t.shape[1] != width or \
+            (width > 1 and t.stride(1) != 1):
+        raise ValueError("%s: %s must be %s [T, %d] with unit column stride on cuda:%d, not %s %s %s"
+                         % (where, name, dtype, width, device, t.dtype, tuple(t.shape), t.device))
+    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else max(t.stride(0), (width + 7) // 8 * 8)
+
+
+def _dense(t, name: str, device: int, shape, dtype, where: str) -> int:
+    if t.dtype != dtype or t.get_device() != device or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError("%s: %s must be contiguous %s %s on cuda:%d, not %s %s %s"
+                         % (where, name, dtype, tuple(shape), device, t.dtype, tuple(t.shape), t.device))
+    return t.data_ptr()
+
+
+def _stream_on(stream, device: int) -> int:
+    """The stream argument of a call on `device`; the current stream of that device by default."""
+    if stream is None:
+        import torch
+        return torch.cuda.current_stream(device).cuda_stream
+    return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+def lora_kv_bytes_required(n_layers: int, n_pages: int, page_tokens: int, n_kv_heads: int, head_dim: int,
+                           kv_type: int) -> int:
+    return int(_lib.lora_kv_bytes_required(n_layers, n_pages, page_tokens, n_kv_heads, head_dim, kv_type))
+
+
+def lora_kv_create(device: int, n_layers: int, n_pages: int, page_tokens: int, n_kv_heads: int, head_dim: int,
+                   kv_type: int, kv_mem) -> KvHandle:
+    """A paged key/value cache over the device tensor `kv_mem`."""
+    if kv_mem.get_device() != device or not kv_mem.is_contiguous():
+        raise ValueError("lora_kv_create: kv_mem must be contiguous on cuda:%d" % device)
+    out = _P()
+    _check(_lib.lora_kv_create(ctypes.byref(out), device, n_layers, n_pages, page_tokens, n_kv_heads, head_dim, kv_type,
+                               kv_mem.data_ptr(), kv_mem.numel() * kv_mem.element_size()), "lora_kv_create")
+    return KvHandle(out.value, device, kv_mem, n_layers, n_pages, page_tokens, n_kv_heads, head_dim, kv_type)
+
+
+def lora_kv_destroy(kv: KvHandle) -> None:
+    if kv.ptr:
+        _check(_lib.lora_kv_destroy(kv), "lora_kv_destroy")
+        kv.ptr = 0
+
+
+def lora_kv_get_error(kv: KvHandle, stream=None) -> int:
+    st = _I(0)
+    _check(_lib.lora_kv_get_error(kv, ctypes.byref(st), _stream_on(stream, kv.device)), "lora_kv_get_error")
+    return int(st.value)
+
+
+def _kv_rows(fn, where: str, kv: KvHandle, layer: int, k, v, page_table, seq_lens, row_offsets, stream) -> None:
+    import torch
+    dev, width, T, n = kv.device, kv.n_kv_heads * kv.head_dim, k.shape[0], seq_lens.shape[0]
+    if v.shape[0] != T or page_table.dim() != 2:
+        raise ValueError("%s: k and v must have the same rows, page_table [n_seqs, max_pages]" % where)
+    kp, ldk = _rows(k, "k", dev, width, torch.bfloat16, where)
+    vp, ldv = _rows(v, "v", dev, width, torch.bfloat16, where)
+    table = _dense(page_table, "page_table", dev, (n, page_table.shape[1]), torch.int32, where)
+    lens = _dense(seq_lens, "seq_lens", dev, (n,), torch.int32, where)
+    off = None if row_offsets is None else _dense(row_offsets, "row_offsets", dev, (n + 1,), torch.int32, where)
+    _check(fn(kv, layer, kp, ldk, vp, ldv, table, page_table.shape[1], lens, off, n, T, _stream_on(stream, dev)), where)
+
+
+def lora_kv_append(kv: KvHandle, layer: int, k, v, page_table, seq_lens, row_offsets=None, stream=None) -> None:
+    """New tokens into the cache: k, v bf16 [T, n_kv_heads * head_dim] (column slices of wider rows will do),
+    page_table int32 [n_seqs, max_pages], seq_lens int32 [n_seqs] (these tokens included), row_offsets int32
+    [n_seqs + 1] or None for one row per sequence."""
+    _kv_rows(_lib.lora_kv_append, "lora_kv_append", kv, layer, k, v, page_table, seq_lens, row_offsets, stream)
+
+
+def lora_kv_gather(kv: KvHandle, layer: int, k, v, page_table, seq_lens, row_offsets=None, stream=None) -> None:
+    """Held tokens back into k, v (bf16): the converse of lora_kv_append."""
+    _kv_rows(_lib.lora_kv_gather, "lora_kv_gather", kv, layer, k, v, page_table, seq_lens, row_offsets, stream)
+
+
+def lora_attend_workspace_bytes(kv: KvHandle, n_heads: int) -> int:
+    return int(_lib.lora_attend_workspace_bytes(kv, n_heads))
+
+
+def lora_attend(kv: KvHandle, layer: int, q, out, page_table, seq_lens, ws, scale: Optional[float] = None,
+                window: int = 0, sinks=None, lse=None, stream=None) -> None:
+    """Attention of one new token per sequence over the cache: q, out bf16 [n_seqs, n_heads * head_dim]; scale
+    1 / sqrt(head_dim) by default; sinks fp32 [n_heads] or None; lse fp32 [n_seqs, n_heads] or None."""
+    import torch
+    dev, n, width = kv.device, seq_lens.shape[0], q.shape[-1]
+    where, n_heads = "lora_attend", width // kv.head_dim
+    if width % kv.head_dim or q.shape[0] != n or out.shape[0] != n or page_table.dim() != 2:
+        raise ValueError("%s: q and out must be [n_seqs, n_heads * head_dim], page_table [n_seqs, max_pages]" % where)
+    qp, ldq = _rows(q, "q", dev, width, torch.bfloat16, where)
+    op, ldo = _rows(out, "out", dev, width, torch.bfloat16, where)
+    table = _dense(page_table, "page_table", dev, (n, page_table.shape[1]), torch.int32, where)
+    lens = _dense(seq_lens, "seq_lens", dev, (n,), torch.int32, where)
+    sp = None if sinks is None else _dense(sinks, "sinks", dev, (n_heads,), torch.float32, where)
+    lp = None if lse is None else _dense(lse, "lse", dev, (n, n_heads), torch.float32, where)
+    wp = _dense(ws, "ws", dev, (ws.numel(),), torch.uint8, where)
+    _check(_lib.lora_attend(kv, layer, qp, ldq, op, ldo, lp, sp, n_heads, table, page_table.shape[1], lens, n,
+                            kv.head_dim ** -0.5 if scale is None else scale, window, wp, ws.numel(),
+                            _stream_on(stream, dev)), where)
+
+
+def lora_rmsnorm(x, weight, eps: float, residual=None, residual_out=None, y=None, q=None, q_scales=None,
+                 stream=None) -> None:
+    """h = x + residual and its root-mean-square norm: h to residual_out, the norm to y (bf16) and / or q
+    (float8_e4m3fn) with q_scales fp32 [T] (one per row) or [T, d / group]."""
+    import torch
+    where, dev, (T, d), bf16 = "lora_rmsnorm", x.get_device(), x.shape, torch.bfloat16
+    xp, ldx = _rows(x, "x", dev, d, bf16, where)
+    wp = _dense(weight, "weight", dev, (d,), bf16, where)
+    ptr, ld = [None] * 4, [0] * 4
+    for i, (t, name, kind) in enumerate(((residual, "residual", bf16), (residual_out, "residual_out", bf16),
+                                         (y, "y", bf16), (q, "q", torch.float8_e4m3fn))):
+        if t is not None:
+            if t.shape[0] != T:
+                raise ValueError("%s: %s must have x's %d rows" % (where, name, T))
+            ptr[i], ld[i] = _rows(t, name, dev, d, kind, where)
+    group, sp = 0, None
+    if q is not None:
+        if q_scales is None:
+            raise ValueError("%s: q needs q_scales" % where)
+        if q_scales.dim() == 2:
+            n = q_scales.shape[1]
+            if n < 1 or d % n:
+                raise ValueError("%s: q_scales must be [T] or [T, d / group]" % where)
+            group = d // n
+            sp = _dense(q_scales, "q_scales", dev, (T, n), torch.float32, where)
+        else:
+            sp = _dense(q_scales, "q_scales", dev, (T,), torch.float32, where)
+    _check(_lib.lora_rmsnorm(dev, xp, ldx, ptr[0], ld[0], ptr[1], ld[1], wp, eps, ptr[2], ld[2], ptr[3], ld[3], sp, group,
+                             T, d, _stream_on(stream, dev)), where)
 
 
 def lora_get_error(pool: PoolHandle, stream=None) -> int:

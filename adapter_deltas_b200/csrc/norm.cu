@@ -1,0 +1,240 @@
+// norm.cu -- the residual's addition and the root-mean-square norm before an
+// adapted projection, in one pass:
+//     h = x + residual,  n = h / sqrt(mean(h^2) + eps) * weight,
+// written as bf16(h) (the next residual), bf16(n) (the rows that lora_linear
+// and lora_apply read) and e4m3 codes of n with one fp32 scale per row or per
+// group of columns (the rows of a base product in 8 bits; quantisation as the
+// key/value cache's, kv.cuh).  h and n stay in fp32 between the roundings: a
+// row is read once into registers, and every output is rounded once from them.
+//
+// Bound by HBM: 9 bytes per element in the full form.  A row is held by `tpr`
+// threads, VPT 16-byte vectors each, vector lane + i * tpr to keep the loads
+// contiguous; rows of at most 32 vectors share a warp, longer ones take whole
+// warps that meet in shared memory once for the sum of squares and, with a
+// scale per row, once for the largest magnitude.  A group's lanes are
+// neighbours in a warp, so its scale needs shuffles only.
+#include "kv.cuh"
+
+namespace lora {
+
+constexpr int kNormMaxThreads = 1024;
+constexpr int kNormMaxVpt = 4;
+constexpr int kNormMaxWidth = 8 * kNormMaxThreads * kNormMaxVpt;
+
+struct NormArgs {
+  const uint8_t *x, *res, *weight;
+  uint8_t *sum, *y, *q;
+  float *scales;
+  long long ldx, ldr, lds, ldy, ldq;  // bytes
+  float eps;
+  int group;  // 0: one scale per row
+  int T, d;
+  int tpr;    // threads per row
+};
+
+template <int VPT>
+__global__ void __launch_bounds__(kNormMaxThreads) rmsnorm_kernel(NormArgs a) {
+  __shared__ float part[32];
+  __shared__ uint32_t peak[32];
+  const int slot = threadIdx.x / a.tpr, lane = threadIdx.x - slot * a.tpr;
+  const long long row = (long long)blockIdx.x * (blockDim.x / a.tpr) + slot;
+  const int nv = a.d / 8, nw = a.tpr / 32;  // nw: warps of a row (0 when rows share one)
+  const bool live = row < a.T;
+  griddep_wait();
+  griddep_launch_dependents();
+  float h[VPT][8];
+  uint4 xs[VPT], rs[VPT], w[VPT];
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int v = lane + i * a.tpr;
+    xs[i] = rs[i] = w[i] = make_uint4(0, 0, 0, 0);
+    if (live && v < nv) {
+      w[i] = __ldg(reinterpret_cast<const uint4 *>(a.weight) + v);
+      xs[i] = *reinterpret_cast<const uint4 *>(a.x + row * a.ldx + v * 16);
+      if (a.res) rs[i] = *reinterpret_cast<const uint4 *>(a.res + row * a.ldr + v * 16);
+    }
+  }
+  float ss = 0.f;
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    float r[8];
+    unpack8(xs[i], h[i]);
+    unpack8(rs[i], r);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      h[i][e] += r[e];
+      ss = fmaf(h[i][e], h[i][e], ss);
+    }
+  }
+  const int width = min(a.tpr, 32);
+  for (int d = width / 2; d; d >>= 1) ss += __shfl_xor_sync(~0u, ss, d);
+  if (nw > 1) {
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = ss;
+    __syncthreads();
+    ss = 0.f;
+    for (int i = 0; i < nw; ++i) ss += part[slot * nw + i];
+  }
+  const float inv = __fdiv_rn(1.f, __fsqrt_rn(ss / a.d + a.eps));
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int v = lane + i * a.tpr;
+    if (live && v < nv && a.sum)
+      *reinterpret_cast<uint4 *>(a.sum + row * a.lds + v * 16) =
+          make_uint4(pack_bf16x2(h[i][0], h[i][1]), pack_bf16x2(h[i][2], h[i][3]), pack_bf16x2(h[i][4], h[i][5]),
+                     pack_bf16x2(h[i][6], h[i][7]));
+    float g[8];
+    unpack8(w[i], g);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) h[i][e] = h[i][e] * inv * g[e];
+    if (live && v < nv && a.y)
+      *reinterpret_cast<uint4 *>(a.y + row * a.ldy + v * 16) =
+          make_uint4(pack_bf16x2(h[i][0], h[i][1]), pack_bf16x2(h[i][2], h[i][3]), pack_bf16x2(h[i][4], h[i][5]),
+                     pack_bf16x2(h[i][6], h[i][7]));
+  }
+  if (!a.q) return;  // (the same for the whole grid)
+  uint32_t m[VPT];
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    m[i] = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) m[i] = max(m[i], lane + i * a.tpr < nv ? abs_bits(h[i][e]) : 0u);
+  }
+  if (a.group) {
+    for (int d = a.group / 16; d; d >>= 1)
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) m[i] = max(m[i], __shfl_xor_sync(~0u, m[i], d));
+  } else {
+#pragma unroll
+    for (int i = 1; i < VPT; ++i) m[0] = max(m[0], m[i]);
+    for (int d = width / 2; d; d >>= 1) m[0] = max(m[0], __shfl_xor_sync(~0u, m[0], d));
+    if (nw > 1) {
+      if ((threadIdx.x & 31) == 0) peak[threadIdx.x >> 5] = m[0];
+      __syncthreads();
+      m[0] = 0;
+      for (int i = 0; i < nw; ++i) m[0] = max(m[0], peak[slot * nw + i]);
+    }
+#pragma unroll
+    for (int i = 1; i < VPT; ++i) m[i] = m[0];
+  }
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int v = lane + i * a.tpr;
+    if (!live || v >= nv) continue;
+    const Quant q = quant_of<448>(__uint_as_float(m[i]));
+    *reinterpret_cast<uint2 *>(a.q + row * a.ldq + v * 8) =
+        make_uint2(code4<LORA_KV_E4M3>(h[i], q), code4<LORA_KV_E4M3>(h[i] + 4, q));
+    if (a.group) {
+      if (v % (a.group / 8) == 0) a.scales[row * (a.d / a.group) + v / (a.group / 8)] = q.scale;
+    } else if (v == 0) {
+      a.scales[row] = q.scale;
+    }
+  }
+}
+
+template <int VPT>
+static int launch_norm(const NormArgs &a, int rows_per_block, cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((a.T + rows_per_block - 1) / rows_per_block));
+  cfg.blockDim = dim3(a.tpr * rows_per_block);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0] = pdl_attribute();
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const int rc = cuda_status(cudaLaunchKernelEx(&cfg, rmsnorm_kernel<VPT>, a));
+  if (rc == LORA_OK) g_launches.fetch_add(1);
+  return rc;
+}
+
+// Operands that are written must not share bytes with one another or with the
+// weight; an output may be an input's own rows (same address and pitch: a row
+// is in registers before any of it is written) but not overlap it otherwise.
+struct NormRows {
+  const void *p;
+  size_t ld, width;
+};
+static bool clash(const NormRows &out, const NormRows &in, int T) {
+  if (out.p && out.p == in.p && out.ld == in.ld) return false;
+  return rows_overlap(out.p, out.ld, out.width, T, in.p, in.ld, in.width, T);
+}
+
+}  // namespace lora
+
+using namespace lora;
+
+extern "C" {
+
+int lora_rmsnorm(int device, const void *x, int ldx, const void *residual, int ldr, void *residual_out, int ldro,
+                 const void *weight, float eps, void *y, int ldy, void *q, int ldq, float *q_scales, int group, int T,
+                 int d, void *stream) {
+  NvtxRange nvtx_range("lora_rmsnorm");
+  if (T < 0 || T > kMaxTokens || d < 8 || d > kNormMaxWidth || !(eps >= 0.f)) return LORA_ERR_INVALID_ARG;
+  if (d % 8) return LORA_ERR_ALIGNMENT;
+  if (group < 0 || (group && (group < 16 || group > 256 || (group & (group - 1)) || d % group)))
+    return LORA_ERR_INVALID_ARG;
+  if (T == 0) return LORA_OK;
+  if (!x || !weight || (!y && !q) || (q && !q_scales)) return LORA_ERR_INVALID_ARG;
+  if (ldx < d || (residual && ldr < d) || (residual_out && ldro < d) || (y && ldy < d) || (q && ldq < d))
+    return LORA_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(weight) || !aligned16(residual) || !aligned16(residual_out) || !aligned16(y) ||
+      !aligned16(q) || (reinterpret_cast<uintptr_t>(q_scales) & 3))
+    return LORA_ERR_ALIGNMENT;
+  if (ldx % 8 || (residual && ldr % 8) || (residual_out && ldro % 8) || (y && ldy % 8) || (q && ldq % 8))
+    return LORA_ERR_ALIGNMENT;
+  const size_t w2 = size_t(d) * 2;
+  const NormRows in[2] = {{x, size_t(ldx) * 2, w2}, {residual, size_t(ldr) * 2, w2}};
+  const size_t n_scales = size_t(T) * (group ? d / group : 1) * 4;
+  const NormRows out[4] = {{residual_out, size_t(ldro) * 2, w2}, {y, size_t(ldy) * 2, w2}, {q, size_t(ldq), size_t(d)},
+                           {q ? q_scales : nullptr, 0, n_scales}};
+  for (int i = 0; i < 4; ++i) {
+    const int rows = i == 3 ? 1 : T;
+    if (rows_overlap(out[i].p, out[i].ld, out[i].width, rows, weight, 0, w2, 1)) return LORA_ERR_INVALID_ARG;
+    for (int k = 0; k < 2; ++k)
+      if (i == 3 ? rows_overlap(out[i].p, 0, n_scales, 1, in[k].p, in[k].ld, in[k].width, T) : clash(out[i], in[k], T))
+        return LORA_ERR_INVALID_ARG;
+    for (int k = 0; k < i; ++k)
+      if (rows_overlap(out[i].p, out[i].ld, out[i].width, rows, out[k].p, out[k].ld, out[k].width, T))
+        return LORA_ERR_INVALID_ARG;
+  }
+  int n_dev = 0;
+  if (cuda_status(cudaGetDeviceCount(&n_dev)) != LORA_OK) return LORA_ERR_CUDA;
+  if (device < 0 || device >= n_dev) return LORA_ERR_INVALID_ARG;
+
+  NormArgs a;
+  a.x = static_cast<const uint8_t *>(x);
+  a.res = static_cast<const uint8_t *>(residual);
+  a.weight = static_cast<const uint8_t *>(weight);
+  a.sum = static_cast<uint8_t *>(residual_out);
+  a.y = static_cast<uint8_t *>(y);
+  a.q = static_cast<uint8_t *>(q);
+  a.scales = q_scales;
+  a.ldx = 2ll * ldx;
+  a.ldr = 2ll * ldr;
+  a.lds = 2ll * ldro;
+  a.ldy = 2ll * ldy;
+  a.ldq = ldq;
+  a.eps = eps;
+  a.group = group;
+  a.T = T;
+  a.d = d;
+  const int nv = d / 8;
+  DeviceGuard g(device);
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (nv <= 32) {  // rows share a warp
+    a.tpr = 2;
+    while (a.tpr < nv) a.tpr *= 2;
+    return launch_norm<1>(a, 256 / a.tpr, st);
+  }
+  if (nv <= 512) {
+    a.tpr = (nv + 31) / 32 * 32;
+    return launch_norm<1>(a, 1, st);
+  }
+  if (nv <= 2 * kNormMaxThreads) {
+    a.tpr = ((nv + 1) / 2 + 31) / 32 * 32;
+    return launch_norm<2>(a, 1, st);
+  }
+  a.tpr = ((nv + 3) / 4 + 31) / 32 * 32;
+  return launch_norm<4>(a, 1, st);
+}
+
+}  // extern "C"

@@ -531,6 +531,154 @@ LORA_API int lora_apply_noalloc(lora_pool *pool, int target, const void *x, int 
                                 int ldy, const int32_t *ids, const float *scales, int T,
                                 void *stream);
 
+/* ------------------------------------------- the key/value cache of a step */
+
+/*
+ * Between the adapted projections of a decode step: keys and values of the
+ * requests' tokens in pages of caller-owned device memory, located through a
+ * page table -- the unified paging of "Multi-LoRA Serving: Sharing One GPU
+ * Across Adapters" (section "How S-LoRA Proved the Model"), where cache pages
+ * live beside adapter pages.  The caller owns the table and hands out pages.
+ *
+ * A cache is n_layers x n_pages pages of page_tokens tokens x n_kv_heads heads
+ * x head_dim, held as kv_type: bf16 as it comes, or 8-bit codes with one fp32
+ * scale per token, head and K or V:
+ *     scale = amax / qmax,  code = round_to_nearest_even(x * qmax / amax),
+ * amax = max |x| over the head's row, qmax = 448 (e4m3) or 127 (int8); the
+ * value held is code * scale.  A row with amax < 2^-100 is held as zeros; one
+ * with an infinity or a NaN reads back as NaN.
+ */
+enum {
+    LORA_KV_BF16 = 0,
+    LORA_KV_E4M3 = 1,
+    LORA_KV_INT8 = 2
+};
+
+/* Opaque cache handle; owns a status word, not the page memory.  Calls on one
+ * handle may run on several streams at once as long as they touch different
+ * tokens (and different workspaces). */
+typedef struct lora_kv lora_kv;
+
+/* Bytes of page memory of a cache (0 on bad arguments).
+ *   n_layers     1..4096
+ *   n_pages      pages per layer
+ *   page_tokens  a power of two, 16..1024
+ *   n_kv_heads   1..1024
+ *   head_dim     a multiple of 16, 16..256
+ *   kv_type      LORA_KV_* */
+LORA_API size_t lora_kv_bytes_required(int n_layers, int n_pages, int page_tokens, int n_kv_heads, int head_dim,
+                              int kv_type);
+
+/* Create a cache over kv_mem: device memory of `device`, 256-byte aligned, at
+ * least lora_kv_bytes_required bytes (not cleared: a token is written before
+ * it is read).  Returns LORA_OK and *out, or an error (nothing allocated). */
+LORA_API int lora_kv_create(lora_kv **out, int device, int n_layers, int n_pages, int page_tokens, int n_kv_heads,
+                   int head_dim, int kv_type, void *kv_mem, size_t kv_bytes);
+
+/* Synchronise the device and free the handle (kv_mem stays the caller's). */
+LORA_API int lora_kv_destroy(lora_kv *kv);
+
+/* As lora_get_error, for a cache's calls. */
+LORA_API int lora_kv_get_error(lora_kv *kv, int *device_status, void *stream);
+
+/*
+ * Write the keys and values of new tokens into a layer of the cache.
+ *   k, ldk       device bf16 [T, ldk], ldk >= n_kv_heads * head_dim: one row per
+ *                token, head after head (a column slice of a fused q/k/v row
+ *                will do); 16-byte aligned, ldk a multiple of 8
+ *   v, ldv       likewise
+ *   page_table   device int32 [n_seqs, max_pages]: page p of sequence s holds
+ *                its tokens p * page_tokens ..; entries that hold no token of
+ *                the call are not read
+ *   seq_lens     device int32 [n_seqs]: each sequence's length with the call's
+ *                tokens included; -1 (or 0) = no request in this place
+ *   row_offsets  device int32 [n_seqs + 1], not decreasing, inside [0, T]: rows
+ *                row_offsets[s] .. row_offsets[s + 1] - 1 are the last tokens of
+ *                sequence s (none, one or many).  NULL: T == n_seqs and row s is
+ *                the last token of sequence s (decode).
+ * One launch.  Rows outside every segment, and rows of a sequence of length
+ * -1, are skipped.  The sticky LORA_ERR_BAD_ID is raised by a sequence whose
+ * length is below -1, past max_pages or less than its rows (none of them is
+ * written), by a token on a page outside [0, n_pages) (that token is not
+ * written) and by offsets out of order (rows in doubt are skipped).  No two
+ * sequences of a call may share the page of a token that it writes.
+ */
+LORA_API int lora_kv_append(lora_kv *kv, int layer, const void *k, int ldk, const void *v, int ldv,
+                   const int32_t *page_table, int max_pages, const int32_t *seq_lens, const int32_t *row_offsets,
+                   int n_seqs, int T, void *stream);
+
+/*
+ * Read held tokens back as bf16, the values rounded once: the converse of
+ * lora_kv_append with the same arguments, k and v being written (rows that
+ * are skipped or in error keep what they held).  k and v must not overlap;
+ * they may be column slices of one buffer.  One launch.
+ */
+LORA_API int lora_kv_gather(lora_kv *kv, int layer, void *k, int ldk, void *v, int ldv, const int32_t *page_table,
+                   int max_pages, const int32_t *seq_lens, const int32_t *row_offsets, int n_seqs, int T,
+                   void *stream);
+
+/* Workspace of lora_attend with n_heads query heads, for any batch (0 for bad
+ * arguments). */
+LORA_API size_t lora_attend_workspace_bytes(const lora_kv *kv, int n_heads);
+
+/*
+ * Attention of one new token per sequence over the cache (which already holds
+ * that token: lora_kv_append comes first).  For query head h of sequence s,
+ * with key head g = h / (n_heads / n_kv_heads), over the positions j in
+ * [max(0, len - window), len), len = seq_lens[s] (window 0: all):
+ *     score_j = scale * (q[s, h] . k_j),
+ *     out[s, h] = sum_j e^score_j v_j / (sum_j e^score_j + e^sinks[h]),
+ *     lse[s, h] = log of that denominator.
+ *   q, ldq       device bf16 [n_seqs, ldq], ldq >= n_heads * head_dim, as k above
+ *   out, ldo     device bf16 [n_seqs, ldo], written; must not overlap q
+ *   lse          device fp32 [n_seqs, n_heads], or NULL
+ *   sinks        device fp32 [n_heads], or NULL (no such term)
+ *   n_heads      a multiple of n_kv_heads, at most 4096
+ *   page_table, max_pages, seq_lens  as for lora_kv_append
+ *   scale        > 0, at most 2^100 (usually 1 / sqrt(head_dim))
+ *   ws, ws_bytes device workspace of lora_attend_workspace_bytes, 16-byte
+ *                aligned; its content need not survive between calls, and calls
+ *                that may overlap on the GPU need one each
+ * fp32 accumulation and statistics; out is rounded once.  A sequence of length
+ * 0 gets zeros (lse: its sink, or minus infinity), one of length -1 keeps its
+ * rows as they were, and so does one whose length is below -1 or past
+ * max_pages, which raises the sticky LORA_ERR_BAD_ID.  Tokens on a page
+ * outside [0, n_pages) are left out of the sums and raise it too.  The result
+ * does not depend on what the pages hold past a sequence's end or before its
+ * window.  Equal inputs give equal bits.
+ */
+LORA_API int lora_attend(lora_kv *kv, int layer, const void *q, int ldq, void *out, int ldo, float *lse,
+                const float *sinks, int n_heads, const int32_t *page_table, int max_pages, const int32_t *seq_lens,
+                int n_seqs, float scale, int window, void *ws, size_t ws_bytes, void *stream);
+
+/* ------------------------------------------ the rows before a projection */
+
+/*
+ * The residual's addition and the root-mean-square norm that make the rows a
+ * projection reads (x of lora_linear / lora_apply), in one launch on `device`:
+ *     h = x + residual,   n = h / sqrt(mean(h^2) + eps) * weight,
+ * h and n kept in fp32, each output rounded once from them.
+ *   x, ldx             device bf16 [T, ldx], ldx >= d
+ *   residual, ldr      device bf16 [T, ldr], or NULL (h = x)
+ *   residual_out, ldro device bf16 [T, ldro]: h, or NULL
+ *   weight             device bf16 [d]
+ *   eps                >= 0
+ *   y, ldy             device bf16 [T, ldy]: n, or NULL
+ *   q, ldq             device e4m3 [T, ldq] (one byte each): the codes of n for a
+ *                      base product in 8 bits, or NULL (y and q not both)
+ *   q_scales, group    device fp32: with group 0 [T], one scale per row; else
+ *                      [T, d / group], one per `group` columns (16, 32, 64, 128
+ *                      or 256, dividing d).  Quantised as the cache's e4m3 rows.
+ *   d                  a multiple of 8, 8..32768
+ * All pointers 16-byte aligned (q_scales 4), all ld* multiples of 8.  An
+ * output may be an input itself (same address and ld: residual_out = residual
+ * updates it in place); otherwise outputs overlap neither inputs nor one
+ * another (LORA_ERR_INVALID_ARG), column slices of one buffer excepted.
+ */
+LORA_API int lora_rmsnorm(int device, const void *x, int ldx, const void *residual, int ldr, void *residual_out,
+                 int ldro, const void *weight, float eps, void *y, int ldy, void *q, int ldq, float *q_scales,
+                 int group, int T, int d, void *stream);
+
 /* ------------------------------------------------------------ diagnostics */
 
 /*
