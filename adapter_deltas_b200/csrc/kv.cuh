@@ -81,8 +81,8 @@ __device__ __forceinline__ long long kv_head_stride(const KvView &kv) {
 // 1990).  From amax 2^64 on both sides are scaled by 2^-64, which keeps the
 // product and the reciprocal in range.  A row whose largest magnitude is below
 // 2^-100 is held as zeros with scale 0 (its scale would lose its bits to
-// underflow); one with an infinity or a NaN has a scale that is not finite,
-// so that all its values read back as NaN.
+// underflow); one with an infinity or a NaN has a NaN for its scale, so that
+// all its values read back as NaN.
 struct Quant {
   float scale;  // what the codes are multiplied by when read
   float mul;    // qmax, times 2^-64 from amax 2^64 on
@@ -94,7 +94,7 @@ template <int QMAX>
 __device__ __forceinline__ Quant quant_of(float amax) {
   Quant q;
   const bool none = amax < 0x1p-100f, big = amax >= 0x1p64f;
-  q.scale = none ? 0.f : __fdiv_rn(amax, (float)QMAX);
+  q.scale = none ? 0.f : fmaf(amax, 0.f, __fdiv_rn(amax, (float)QMAX));  // (infinity * 0: NaN)
   q.amax = big ? amax * 0x1p-64f : amax;
   q.mul = none ? 0.f : big ? QMAX * 0x1p-64f : (float)QMAX;
   q.rcp = none ? 0.f : __frcp_rn(q.amax);
