@@ -26,16 +26,17 @@
 //    what a block's border cuts goes to the workspace and is joined by a second,
 //    small launch (again in order: equal inputs give equal bits).
 //
-// The products run on the warp-level tensor instruction (m16n8k16, bf16): a
-// unit's 8 query heads are few rows, and tcgen05 takes no fewer than 64.  With
-// at most 8 heads the 16 rows carry each head twice; for the scores both copies
-// give the same number, and for the values the first copy multiplies the bf16
-// rounding of the weights and the second what the rounding left, so that the
-// weights keep about 16 bits at no further instruction (rounded weights alone
-// would add an error of the size of the result's own rounding).  With 9 to 16
-// heads the rows are all different and the rest is a second instruction.
-// 8-bit codes become bf16 exactly, with integer instructions on four at a time;
-// the scales of K multiply the scores, those of V the weights, in fp32.
+// The products run on the warp-level tensor instruction (m16n8k16): a unit's 8
+// query heads are the N = 8 of both products, S^T = K q^T (16 tokens x 8 heads)
+// and O^T += V^T P^T (16 dims x 8 heads), K and V read from the staged tile as the
+// A operand.  (With the heads as M half of each instruction and of the
+// accumulators would be padding; tcgen05 takes no fewer than 64 rows.)  The
+// weights leave S^T token by token and are needed head by head: one movmatrix
+// per 8 x 8 block turns them.  They enter as two terms, the leading bits and the
+// rest: rounded weights alone would add an error of the size of the result's
+// own rounding.  8-bit codes are multiplied as they are (int8 keys) or become
+// fp16 exactly, in 3 to 5 instructions per four; K's scales multiply the
+// scores, V's the weights, in fp32.
 //
 // Tokens outside the range get weight 0 by selection, not by adding: what lies
 // in their places (the end of a page, before the window) may be anything.
@@ -43,10 +44,11 @@
 
 namespace lora {
 
-constexpr int kAttMaxWarps = 8;
+constexpr int kAttMaxWarps = 12;
 constexpr int kAttMaxStages = 8;
 constexpr int kAttSmem = 227 * 1024;
 constexpr int kJoinThreads = 512;
+constexpr int kSlack = 4, kVSlack = 2;  // powers of two
 
 struct AttendArgs {
   const uint8_t *q;
@@ -85,6 +87,12 @@ __device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                : "r"(addr));
 }
+// 8 x 8 of 16-bit values, transposed: a thread has two neighbours of a row.
+__device__ __forceinline__ uint32_t turn(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
   asm volatile(
@@ -92,6 +100,7 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+__device__ constexpr float exp2_int(int e) { return (float)(1 << e); }
 __device__ __forceinline__ float exp2_fast(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -102,13 +111,6 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
                                         uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ void mma_e4m3(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                         uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
@@ -141,25 +143,35 @@ __device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t &even, uint32_
   }
 }
 
+// A word of K codes as two fp16 pairs: e4m3 bytes 0, 1 and 2, 3 (one instruction
+// each); int8 bytes 0, 2 and 1, 3.
+template <int TYPE>
+__device__ __forceinline__ void key_codes_to_f16(uint32_t w, uint32_t &a, uint32_t &b) {
+  if (TYPE == LORA_KV_E4M3)
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+        : "=r"(a), "=r"(b)
+        : "r"(w));
+  else
+    codes_to_f16<TYPE>(w, a, b);
+}
+
 // How the scores of a unit are formed.
 //  kBf16: q as it is, times bf16 keys.
-//  kE4m3: q (scaled per head by a power of two to at most 256) as hi + lo / 32, both
-//         e4m3: exact down to 2^-14 of the head's largest |q|, below that off by at
-//         most 2^-23 of it.  Keys are multiplied as the codes they are.
+//  kF16:  q scaled per head by a power of two to below 2, as fp16: exact down to
+//         2^-14 of the head's largest |q|, below that off by at most 2^-25 of it.
+//         Keys become fp16 exactly.  (The warp-level product of e4m3 operands is
+//         no single instruction of this GPU: it took 1.7 times the instructions
+//         of this form.)
 //  kInt8: q = (hi + lo / 128 + rest / 16384) * amax / 127, all int8: off by at most
-//         2^-22 of the largest |q|.  Products and sums are exact.
-//  kF16:  q scaled by a power of two to fp16 (as exact as kE4m3), int8 keys as
-//         fp16; with 9 to 16 heads, where three products of int8 would take more
-//         registers than there are.
-// hi and lo of the two 8-bit forms share an instruction while a unit has at
-// most 8 heads: rows 0-7 are hi, rows 8-15 lo.
-enum { kBf16, kE4m3, kInt8, kF16 };
-__host__ __device__ constexpr int score_form(int type, bool wide) {
-  return type == LORA_KV_BF16 ? kBf16 : type == LORA_KV_E4M3 ? kE4m3 : wide ? kF16 : kInt8;
+//         2^-22 of the largest |q|.  Keys are multiplied as the codes they are;
+//         products and sums are exact.  (Not for 9 to 16 heads wider than 128: the
+//         three terms would take more registers than there are.)
+enum { kBf16, kF16, kInt8 };
+__host__ __device__ constexpr int score_form(int type, int dim, int nt) {
+  return type == LORA_KV_BF16 ? kBf16 : type == LORA_KV_INT8 && (nt == 1 || dim <= 128) ? kInt8 : kF16;
 }
-__host__ __device__ constexpr int q_regs(int form, int nb, bool wide) {
-  const int pairs = (nb + 1) / 2;
-  return form == kE4m3 ? pairs * (wide ? 8 : 4) : form == kInt8 ? pairs * 6 : nb * (wide ? 4 : 2);
+__host__ __device__ constexpr int q_regs(int form, int nb, int nt) {  // per n-tile: 6 for two blocks, or 2 a block
+  return nt * (form == kInt8 ? (nb + 1) / 2 * 6 : nb * 2);
 }
 
 // Length of sequence s where it is one that is attended to, else 0 (none, empty, in error).
@@ -168,10 +180,11 @@ __device__ __forceinline__ int seq_len(const KvView &kv, const KvSeqs &s, int i)
   return len > 0 && len <= ((long long)s.max_pages << kv.log2_page) ? len : 0;
 }
 __device__ __forceinline__ int first_token(int len, int window) { return window && len > window ? len - window : 0; }
-// Steps of a unit of a sequence: its tiles from the first token's to the last one's.
+// Steps of a unit of a sequence, of tt tiles each and aligned to that: from the
+// first token's to the last one's.
 __device__ __forceinline__ int seq_steps(int len, int window, int tt) {
-  const int tiles = (len + kTileTokens - 1) / kTileTokens - first_token(len, window) / kTileTokens;
-  return (tiles + tt - 1) / tt;
+  const int per = kTileTokens * tt;
+  return (len + per - 1) / per - first_token(len, window) / per;
 }
 
 // Write row r's result from its state: o = sums for 4 dims, m and l over all tokens.
@@ -194,27 +207,26 @@ __device__ __forceinline__ Ends finish(const AttendArgs &a, int head, float m, f
 
 // ------------------------------------------------------------------ kernel
 
-// What a stage of a ring holds.
+// What a stage of a ring holds (written for the first step of a unit or range).
 struct Step {
   int seq, unit, pos, len;  // sequence, unit, first token of the step, tokens of the sequence
 };
 
 // DIM: the head's width, or with ANY the largest of a range of multiples of 16 (kv.dim is the width).
-// TT: tiles of 16 tokens per step.  WIDE: 9..16 query heads to a unit (else up to 8).
-template <int TYPE, int DIM, bool ANY, int TT, bool WIDE>
-__global__ void __launch_bounds__(kAttMaxWarps * 32, 1) attend_kernel(KvView kv, KvSeqs s, AttendArgs a) {
+// TT: tiles of 16 tokens per step.  WARPS: most warps of a block.  NT: 8 NT query heads to a unit.
+template <int TYPE, int DIM, bool ANY, int TT, int WARPS, int NT>
+__global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(KvView kv, KvSeqs s, AttendArgs a) {
   constexpr int ES = kv_elt(TYPE);
-  constexpr int ROWS = WIDE ? 16 : 8;   // query heads of a unit
-  constexpr int HALVES = WIDE ? 2 : 1;  // of which a thread has one or two
+  constexpr int ROWS = 8 * NT;          // query heads of a unit
   constexpr int NB = DIM / 16;          // blocks of 16 dims
   const int dim = ANY ? kv.dim : DIM, nb = ANY ? kv.dim / 16 : NB;
   const int row_bytes = dim * ES, chunks = row_bytes / 16;
+  constexpr int kStep = kTileTokens * TT;  // tokens of a step
   const int tile_bytes = kv_tile_bytes(TYPE, dim), stage_bytes = TT * tile_bytes;
 
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint64_t full[kAttMaxWarps][kAttMaxStages];
   __shared__ Step held[kAttMaxWarps][kAttMaxStages];
-  __shared__ int bad_tiles[kAttMaxWarps][kAttMaxStages];  // bit i: tile i of the stage is on no page of the cache
   __shared__ long long scan[kAttMaxWarps], from[kAttMaxWarps];  // from: a warp's first step, from its sequence's first
   __shared__ int2 start[kAttMaxWarps];                          // {sequence, length} of it
   __shared__ int4 piece[2 * kAttMaxWarps];  // [2 warp + which]: {sequence (-1: none), unit, cut before 1 / after 2, -}
@@ -295,49 +307,62 @@ __global__ void __launch_bounds__(kAttMaxWarps * 32, 1) attend_kernel(KvView kv,
     // ---- fetching side: the next step to fetch, and pages of up to 32 tiles
     int left = count;  // steps not yet fetched
     int fseq = start[warp].x, flen = start[warp].y;
-    int fsteps = seq_steps(flen, a.window, TT), ft0 = first_token(flen, a.window) / kTileTokens;
-    int funit, fstep;
+    int funit, fpos;   // fpos: first token of the step
     {
+      const int n = seq_steps(flen, a.window, TT);
       const unsigned long long off = from[warp];
+      int step;
       if (off >> 32) {
-        funit = (int)(off / (unsigned)fsteps);
-        fstep = (int)(off - (unsigned long long)funit * fsteps);
+        funit = (int)(off / (unsigned)n);
+        step = (int)(off - (unsigned long long)funit * n);
       } else {
-        funit = (int)((unsigned)off / (unsigned)fsteps);
-        fstep = (int)((unsigned)off - (unsigned)funit * fsteps);
+        funit = (int)((unsigned)off / (unsigned)n);
+        step = (int)((unsigned)off - (unsigned)funit * n);
       }
+      fpos = (first_token(flen, a.window) / kStep + step) * kStep;
     }
-    const bool starts_inside = fstep != 0;  // of its unit
+    const bool starts_inside = fpos > first_token(flen, a.window);  // of its unit
+    bool fnew = true;             // the step to fetch is the first of a unit or of the range
+    int pages = 0, pbase = -1;    // lane j: page of the sequence's tile pbase + j
+    unsigned bad_tiles = 0;       // bits stage * TT ..: tiles of a stage that are on no page of the cache
     const long long head_stride = kv_head_stride(kv);
     const uint8_t *fhead = kv.base + (funit / a.head_groups) * head_stride;
-    int pages = 0, pbase = -1;  // lane j: page of the sequence's tile pbase + j
+    // a step's tiles lie in one page, one behind the other, unless pages are shorter
+    const bool one_copy = TT == 1 || (1 << kv.log2_page) >= kStep;
 
     auto fetch = [&](int stage) {
       if (left <= 0) return;
       --left;
-      const int tiles = (flen + kTileTokens - 1) / kTileTokens;
-      const int t = ft0 + fstep * TT, want = ft0 + (fstep * TT & ~31);
+      const int t = fpos / kTileTokens, want = t & ~31;
       if (want != pbase) {
         pbase = want;
         pages = -1;
-        if (pbase + lane < tiles)
+        if ((pbase + lane) * kTileTokens < flen)
           pages = __ldg(s.table + (long long)fseq * s.max_pages + (((pbase + lane) * kTileTokens) >> kv.log2_page));
       }
-      // lane i fetches tile t + i
-      const int page = TT == 1 ? __shfl_sync(~0u, pages, t - pbase) : __shfl_sync(~0u, pages, (t - pbase + lane) & 31);
-      const bool wanted = lane < TT && t + lane < tiles;
-      const long long at = wanted ? kv_tile_offset(kv, page, (t + lane) * kTileTokens) : -1;
-      const unsigned ok = __ballot_sync(~0u, at >= 0), need = __ballot_sync(~0u, wanted);
+      // tiles [t0, t1) of the step: lane i has tile i (or lane 0 all of them)
+      const int t0 = max(first_token(flen, a.window) / kTileTokens - t, 0);
+      const int t1 = min((flen - fpos + kTileTokens - 1) / kTileTokens, TT);
+      const int mine = one_copy ? t0 : t0 + lane;
+      const int page = __shfl_sync(~0u, pages, (t + mine) & 31);
+      const long long at = kv_tile_offset(kv, page, fpos + mine * kTileTokens);
+      const unsigned ok = __ballot_sync(~0u, at >= 0 && lane < (one_copy ? 1 : t1 - t0));
+      const int n = one_copy ? (ok ? t1 - t0 : 0) : __popc(ok);
       if (lane == 0) {
-        held[warp][stage] = {fseq, funit, t * kTileTokens, flen};
-        bad_tiles[warp][stage] = need & ~ok;
-        mbar_arrive_expect_tx(&full[warp][stage], __popc(ok) * tile_bytes);
-        if (need & ~ok) set_status(kv.status, LORA_ERR_BAD_ID);
+        if (fnew) held[warp][stage] = {fseq, funit, fpos, flen};
+        mbar_arrive_expect_tx(&full[warp][stage], n * tile_bytes);
+      }
+      if (n < t1 - t0) {
+        bad_tiles |= (((1u << t1) - (1u << t0)) & ~(one_copy ? 0u : ok << t0)) << (stage * TT);
+        if (lane == 0) set_status(kv.status, LORA_ERR_BAD_ID);
       }
       __syncwarp();
-      if (at >= 0) bulk_g2s(ring + stage * stage_bytes + lane * tile_bytes, fhead + at, tile_bytes, &full[warp][stage]);
-      if (++fstep == fsteps) {
-        fstep = 0;
+      if (ok >> lane & 1)
+        bulk_g2s(ring + stage * stage_bytes + mine * tile_bytes, fhead + at, one_copy ? n * tile_bytes : tile_bytes,
+                 &full[warp][stage]);
+      fpos += kStep;
+      fnew = fpos >= flen;
+      if (fnew) {
         if (++funit == a.units) {
           funit = 0;
           pbase = -1;
@@ -346,60 +371,60 @@ __global__ void __launch_bounds__(kAttMaxWarps * 32, 1) attend_kernel(KvView kv,
               ++fseq;
               flen = seq_len(kv, s, fseq);
             } while (flen == 0);
-            fsteps = seq_steps(flen, a.window, TT);
-            ft0 = first_token(flen, a.window) / kTileTokens;
           }
         }
+        fpos = first_token(flen, a.window) / kStep * kStep;
         fhead = kv.base + (funit / a.head_groups) * head_stride;
       }
     };
 
     // ---- computing side
     const uint32_t ring32 = smem_u32(ring);
-    const int row = lane >> 2, quad = lane & 3;
-    const int r8 = lane & 7, mat = lane >> 3;  // this lane's row and matrix of an ldmatrix
+    const int g = lane >> 2, j2 = 2 * (lane & 3);  // of a product: its row (token, dim) and its pair of columns (heads)
+    const int r8 = lane & 7, mat = lane >> 3;      // this lane's row and matrix of an ldmatrix
     const int low = chunks & -chunks, grp = low < 8 ? low : 8;
     const int sw = (r8 / (8 / grp)) & (grp - 1);  // its rows' chunk permutation (rows r8 and r8 + 8 share it)
-    // K: bf16 (tokens 0-7 | 8-15) x (dims 0-7 | 8-15); 8-bit (tokens) x (dim blocks 2i | 2i + 1).  V: transposed.
-    const uint32_t k_row = ((TYPE == LORA_KV_BF16 ? mat >> 1 : mat & 1) * 8 + r8) * row_bytes;
-    const int k_c = TYPE == LORA_KV_BF16 ? mat & 1 : mat >> 1;
-    const uint32_t v_row = (kTileTokens + (mat & 1) * 8 + r8) * row_bytes;
-    const int v_c = mat >> 1;
+    // K: (tokens 0-7 | 8-15) x (chunk | next chunk); V, transposed: the same for 8 bits, for bf16 chunks first
+    const uint32_t k_row = ((mat & 1) * 8 + r8) * row_bytes;
+    const uint32_t v_row = (kTileTokens + (TYPE == LORA_KV_BF16 ? mat >> 1 : mat & 1) * 8 + r8) * row_bytes;
+    const int k_c = mat >> 1, v_c = TYPE == LORA_KV_BF16 ? mat & 1 : mat >> 1;
 
-    constexpr int FORM = score_form(TYPE, WIDE);
-    uint32_t qa[q_regs(FORM, NB, WIDE)];
-    float qs[HALVES];  // what a score is multiplied by for q's scaling
-    float o[2 * NB][4], m[HALVES], l[HALVES], vtop = 0.f;  // vtop: largest V scale so far (8 bits)
-    int cseq = -1, cunit = -1;
-    bool cut_before = false;
+    constexpr int FORM = score_form(TYPE, DIM, NT);
+    constexpr int QN = q_regs(FORM, NB, 1);
+    uint32_t qa[NT][QN];
+    float qs[NT][2];  // what a score is multiplied by: the softmax's scale and that of q's terms
+    float o[NT][NB][4], m[NT][2], l[NT][2];
+    float vtop = 0.f, unit = 0.f;  // (8 bits) V's scales: reference, and the weights' unit by it
+    int cseq = -1, cunit = -1, cpos = 0, clen = 0, cfirst = 0;  // of the step to compute; cfirst: the unit's first token
+    bool cut_before = false, cnew = true;
     int stage = 0, fstage = 0;
     uint32_t phase = 0;
 
-    // q as the products' A operand: rows = heads, columns = dims in the order of the K operand
+    // q as the products' B operand: columns = heads, rows = dims in the order of the K operand
     auto load_q = [&]() {
-      const int kvh = cunit / a.head_groups, h0 = (cunit - kvh * a.head_groups) * ROWS;
+      const int kvh = cunit / a.head_groups, h0 = (cunit - kvh * a.head_groups) * ROWS, j = lane & 3;
 #pragma unroll
-      for (int h = 0; h < HALVES; ++h) {
-        const bool live = h0 + row + 8 * h < a.group;
-        const uint8_t *q = a.q + cseq * a.ldq + (long long)(kvh * a.group + h0 + row + 8 * h) * dim * 2;
-        uint2 u[NB];  // bf16: dims 16 b + 2 quad, + 1, + 8, + 9; 8 bits: dims 16 b + 4 quad ..
+      for (int h = 0; h < NT; ++h) {
+        const bool live = h0 + g + 8 * h < a.group;
+        const uint8_t *q = a.q + cseq * a.ldq + (long long)(kvh * a.group + h0 + g + 8 * h) * dim * 2;
+        uint2 u[NB];  // bf16: dims 16 b + 2 j, + 1, + 8, + 9; 8 bits: dims 16 b + 4 j ..
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
           u[b] = make_uint2(0, 0);
           if (!live || (ANY && b >= nb)) continue;
           if (TYPE == LORA_KV_BF16) {
-            u[b].x = __ldg(reinterpret_cast<const uint32_t *>(q + b * 32 + quad * 4));
-            u[b].y = __ldg(reinterpret_cast<const uint32_t *>(q + b * 32 + quad * 4 + 16));
+            u[b].x = __ldg(reinterpret_cast<const uint32_t *>(q + b * 32 + j * 4));
+            u[b].y = __ldg(reinterpret_cast<const uint32_t *>(q + b * 32 + j * 4 + 16));
           } else {
-            u[b] = __ldg(reinterpret_cast<const uint2 *>(q + b * 32 + quad * 8));
+            u[b] = __ldg(reinterpret_cast<const uint2 *>(q + b * 32 + j * 8));
           }
         }
         if (FORM == kBf16) {
-          qs[h] = 1.f;
+          qs[h][0] = qs[h][1] = a.scale2;
 #pragma unroll
           for (int b = 0; b < NB; ++b) {
-            qa[b * 2 * HALVES + h] = u[b].x;
-            qa[b * 2 * HALVES + HALVES + h] = u[b].y;
+            qa[h][b * 2] = u[b].x;
+            qa[h][b * 2 + 1] = u[b].y;
           }
           continue;
         }
@@ -410,54 +435,26 @@ __global__ void __launch_bounds__(kAttMaxWarps * 32, 1) attend_kernel(KvView kv,
         top = max(top, __shfl_xor_sync(~0u, top, 1));
         top = max(top, __shfl_xor_sync(~0u, top, 2));
         const float amax = fmaxf(__uint_as_float(top << 16), 0x1p-100f);  // (a NaN is lost here and comes back below)
-        const float nan = top >= 0x7f80u ? __int_as_float(0x7fc00000) : 0.f;
         const float two = __uint_as_float(__float_as_uint(amax) & 0x7f800000u);  // 2^E, 2^E <= amax
-        if (FORM == kE4m3) {
-          const float mul = 0x1p7f / two;
-          qs[h] = two * 0x1p-7f + nan;
+        const float mul = FORM == kInt8 ? 127.f / amax : 1.f / two;
+        float mine = FORM == kInt8 ? amax * (1.f / (127.f * 16384.f)) : two;
+        mine = top >= 0x7f80u ? __int_as_float(0x7fc00000) : mine * a.scale2;
+        qs[h][0] = __shfl_sync(~0u, mine, 4 * j2);
+        qs[h][1] = __shfl_sync(~0u, mine, 4 * j2 + 4);
 #pragma unroll
-          for (int b = 0; b < NB; ++b) {
-            const float x[4] = {bf16_lo(u[b].x) * mul, bf16_hi(u[b].x) * mul, bf16_lo(u[b].y) * mul, bf16_hi(u[b].y) * mul};
-            const uint32_t hi = e4m3x2(x[0], x[1]) | e4m3x2(x[2], x[3]) << 16;
-            float y[4];
-            decode4<LORA_KV_E4M3>(hi, y);
-            const uint32_t lo = e4m3x2((x[0] - y[0]) * 32.f, (x[1] - y[1]) * 32.f) |
-                                e4m3x2((x[2] - y[2]) * 32.f, (x[3] - y[3]) * 32.f) << 16;
-            const int k = (b >> 1) * 4 * HALVES + (b & 1) * 2;  // a0, a1 | a2, a3 of a pair of blocks
-            if (WIDE) {
-              qa[k + h] = hi;
-              qa[k + 4 + h] = lo;
-            } else {
-              qa[k] = hi;
-              qa[k + 1] = lo;
-            }
-          }
-          if (NB & 1) qa[(NB / 2) * 4 * HALVES + 2] = qa[(NB / 2) * 4 * HALVES + 3] = 0;
-        } else if (FORM == kInt8) {
-          const float mul = 127.f / amax;
-          qs[h] = amax * (1.f / (127.f * 16384.f)) + nan;
-#pragma unroll
-          for (int b = 0; b < NB; ++b) {
-            float x[4] = {bf16_lo(u[b].x) * mul, bf16_hi(u[b].x) * mul, bf16_lo(u[b].y) * mul, bf16_hi(u[b].y) * mul};
-            uint32_t t[3];
+        for (int b = 0; b < NB; ++b) {
+          float x[4] = {bf16_lo(u[b].x) * mul, bf16_hi(u[b].x) * mul, bf16_lo(u[b].y) * mul, bf16_hi(u[b].y) * mul};
+          if (FORM == kInt8) {
 #pragma unroll
             for (int k = 0; k < 3; ++k) {
-              t[k] = int8x4(x[0], x[1], x[2], x[3]);
+              const uint32_t t = int8x4(x[0], x[1], x[2], x[3]);
+              qa[h][(b >> 1) * 6 + 2 * k + (b & 1)] = t;
 #pragma unroll
-              for (int e = 0; e < 4; ++e) x[e] = (x[e] - (float)(int8_t)(t[k] >> (8 * e))) * 128.f;
+              for (int e = 0; e < 4; ++e) x[e] = (x[e] - (float)(int8_t)(t >> (8 * e))) * 128.f;
             }
-            const int k = (b >> 1) * 6 + (b & 1) * 2;
-            qa[k] = t[0];
-            qa[k + 1] = t[1];
-            qa[(b >> 1) * 6 + 4 + (b & 1)] = t[2];
-          }
-        } else {  // kF16
-          const float mul = 1.f / two;
-          qs[h] = two + nan;
-#pragma unroll
-          for (int b = 0; b < NB; ++b) {  // even dims, then odd ones
-            qa[b * 4 + h] = pack_f16x2(bf16_lo(u[b].x) * mul, bf16_lo(u[b].y) * mul);
-            qa[b * 4 + 2 + h] = pack_f16x2(bf16_hi(u[b].x) * mul, bf16_hi(u[b].y) * mul);
+          } else {  // as key_codes_to_f16 pairs the dims
+            qa[h][b * 2] = TYPE == LORA_KV_E4M3 ? pack_f16x2(x[0], x[1]) : pack_f16x2(x[0], x[2]);
+            qa[h][b * 2 + 1] = TYPE == LORA_KV_E4M3 ? pack_f16x2(x[2], x[3]) : pack_f16x2(x[1], x[3]);
           }
         }
       }
@@ -469,14 +466,12 @@ __global__ void __launch_bounds__(kAttMaxWarps * 32, 1) attend_kernel(KvView kv,
       if (++fstage == a.n_stages) fstage = 0;
       if (i < 0) continue;
       const bool end = i == count;
-      Step st = held[warp][stage];
-      if (end || st.seq != cseq || st.unit != cunit) {
+      if (end || cnew) {
         if (cseq >= 0) {
           // The unit's state leaves the registers: as its result when the warp
-          // has seen all of it, else as a piece to be joined.  At the range's
-          // end the fetching side, just past it, tells whether the unit ends
-          // too; the ring is then free for the state.
-          const bool cut_after = end && fstep != 0;
+          // has seen all of it, else as a piece to be joined (at the range's end
+          // the ring is free for it).
+          const bool cut_after = end && !cnew;
           const bool whole = !cut_before && !cut_after;
           const int kvh = cunit / a.head_groups, h0 = (cunit - kvh * a.head_groups) * ROWS;
           float *state = end ? reinterpret_cast<float *>(ring) : a.first_in_smem
@@ -486,62 +481,77 @@ __global__ void __launch_bounds__(kAttMaxWarps * 32, 1) attend_kernel(KvView kv,
             const int k = 2 * warp + (cut_before ? 0 : 1);
             piece[k] = make_int4(cseq, cunit, (cut_before ? 1 : 0) | (cut_after ? 2 : 0), 0);
             where[k] = state;
-            if (cut_after && warp == (wq ? n_warps : wr) - 1) tail_steps = fsteps - fstep;  // (the block's last steps)
+            if (cut_after && warp == (wq ? n_warps : wr) - 1) tail_steps = (clen - cpos + kStep - 1) / kStep;  // (the block's last steps)
           }
 #pragma unroll
-          for (int h = 0; h < HALVES; ++h) {
-            l[h] += __shfl_xor_sync(~0u, l[h], 1);
-            l[h] += __shfl_xor_sync(~0u, l[h], 2);
-            const int r = row + 8 * h, hd = kvh * a.group + h0 + r;
-            if (r >= a.rows || h0 + r >= a.group) continue;
-            float mul = TYPE == LORA_KV_BF16 ? 1.f : vtop * 0x1p-15f;
-            uint8_t *out = a.out + cseq * a.ldo + (long long)hd * dim * 2;
-            if (whole) {
-              const Ends e = finish(a, hd, m[h], l[h]);
-              mul *= e.mul;
-              if (a.lse && quad == 0) a.lse[(long long)cseq * a.n_heads + hd] = e.lse;
-            } else if (quad == 0) {
-              state[r] = m[h];
-              state[a.rows + r] = l[h];
+          for (int h = 0; h < NT; ++h) {
+            float mul[2];
+            bool on[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              l[h][e] += __shfl_xor_sync(~0u, l[h][e], 4);
+              l[h][e] += __shfl_xor_sync(~0u, l[h][e], 8);
+              l[h][e] += __shfl_xor_sync(~0u, l[h][e], 16);
+              const int r = 8 * h + j2 + e, hd = kvh * a.group + h0 + r;
+              on[e] = r < a.rows && h0 + r < a.group;
+              mul[e] = TYPE == LORA_KV_BF16 ? 1.f : vtop / exp2_int(15 - kSlack - kVSlack);
+              if (!on[e]) continue;
+              if (whole) {
+                const Ends x = finish(a, hd, m[h][e], l[h][e]);
+                mul[e] *= x.mul;
+                if (a.lse && g == 0) a.lse[(long long)cseq * a.n_heads + hd] = x.lse;
+              } else if (g == 0) {
+                state[r] = m[h][e];
+                state[a.rows + r] = l[h][e];
+              }
             }
+            const int r = 8 * h + j2;
             float *sums = state + state_head(a.rows) + r * dim;
+            uint8_t *out = a.out + cseq * a.ldo + (long long)(kvh * a.group + h0 + r) * dim * 2;
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
               if (ANY && b >= nb) continue;
-              float x[4];  // n-tiles 2b and 2b + 1, columns 2 quad and 2 quad + 1
+              // a thread's two neighbouring dims of each of its two heads
+              int d = 16 * b + 2 * g;  // 8 bits: rows g and g + 8 are dims 2 g and 2 g + 1
+              float x[2][2];
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const float(&c)[4] = o[2 * b + (e >> 1)];
-                x[e] = (WIDE ? c[(e & 1) + 2 * h] : c[e & 1] + c[(e & 1) + 2]) * mul;
-              }
-              if (TYPE == LORA_KV_BF16) {  // dims 16 b + 2 quad, + 1, + 8, + 9
-                const int d = 16 * b + 2 * quad;
-                if (whole) {
-                  *reinterpret_cast<uint32_t *>(out + d * 2) = pack_bf16x2(x[0], x[1]);
-                  *reinterpret_cast<uint32_t *>(out + d * 2 + 16) = pack_bf16x2(x[2], x[3]);
-                } else {
-                  *reinterpret_cast<float2 *>(sums + d) = make_float2(x[0], x[1]);
-                  *reinterpret_cast<float2 *>(sums + d + 8) = make_float2(x[2], x[3]);
+              for (int e = 0; e < 2; ++e) {
+                x[e][0] = o[h][b][e];
+                x[e][1] = o[h][b][2 + e];
+                if (TYPE == LORA_KV_BF16) {  // dims g and g + 8: neighbouring rows trade
+                  const float got = __shfl_xor_sync(~0u, g & 1 ? x[e][0] : x[e][1], 4);
+                  x[e][0] = g & 1 ? got : x[e][0];
+                  x[e][1] = g & 1 ? x[e][1] : got;
                 }
-              } else {  // n-tile 2b: even dims, 2b + 1: odd dims; 16 b + 4 quad ..
-                const int d = 16 * b + 4 * quad;
+              }
+              if (TYPE == LORA_KV_BF16) d = 16 * b + (g & 1 ? 7 + g : g);
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                if (!on[e]) continue;
                 if (whole)
-                  *reinterpret_cast<uint2 *>(out + d * 2) = make_uint2(pack_bf16x2(x[0], x[2]), pack_bf16x2(x[1], x[3]));
+                  *reinterpret_cast<uint32_t *>(out + (e * dim + d) * 2) = pack_bf16x2(x[e][0] * mul[e], x[e][1] * mul[e]);
                 else
-                  *reinterpret_cast<float4 *>(sums + d) = make_float4(x[0], x[2], x[1], x[3]);
+                  *reinterpret_cast<float2 *>(sums + e * dim + d) = make_float2(x[e][0] * mul[e], x[e][1] * mul[e]);
               }
             }
           }
         }
         if (end) break;
         cut_before = i == 0 && starts_inside;
+        const Step st = held[warp][stage];
         cseq = st.seq;
         cunit = st.unit;
+        cpos = st.pos;
+        clen = st.len;
+        cfirst = first_token(clen, a.window);
 #pragma unroll
-        for (int h = 0; h < HALVES; ++h) m[h] = -INFINITY, l[h] = 0.f;
-        vtop = 0.f;
+        for (int h = 0; h < NT; ++h) {
+          m[h][0] = m[h][1] = -INFINITY;
+          l[h][0] = l[h][1] = 0.f;
 #pragma unroll
-        for (int n = 0; n < 2 * NB; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
+          for (int b = 0; b < NB; ++b) o[h][b][0] = o[h][b][1] = o[h][b][2] = o[h][b][3] = 0.f;
+        }
+        vtop = unit = 0.f;
         load_q();
       }
       if (!mbar_wait_bounded(&full[warp][stage], phase, kv.status)) {
@@ -553,11 +563,15 @@ __global__ void __launch_bounds__(kAttMaxWarps * 32, 1) attend_kernel(KvView kv,
       const uint32_t st32 = ring32 + stage * stage_bytes;
       uint8_t *stp = ring + stage * stage_bytes;
       // tokens of the step that count: [lo, hi) of its 16 TT, without those on bad pages
-      const int lo = first_token(st.len, a.window) - st.pos, hi = st.len - st.pos, bad = bad_tiles[warp][stage];
-      const bool partial = lo > 0 || hi < kTileTokens * TT || bad;
+      const int lo = cfirst - cpos, hi = clen - cpos;
+      const unsigned bad = bad_tiles >> (stage * TT) & ((1u << TT) - 1u);
+      const bool partial = lo > 0 || hi < kStep || bad;
+      bad_tiles &= ~(((1u << TT) - 1u) << (stage * TT));
+      cpos += kStep;
+      cnew = cpos >= clen;
       if (TYPE != LORA_KV_INT8 && partial) {
         // weight 0 times what lies there must be 0: clear V's rows outside (int8 has no NaN)
-        for (int x = lane; x < kTileTokens * TT * chunks; x += 32) {
+        for (int x = lane; x < kStep * chunks; x += 32) {
           const int t = x / chunks;
           if (t >= lo && t < hi && !(bad >> (t / kTileTokens) & 1)) continue;
           *reinterpret_cast<uint4 *>(stp + (t / kTileTokens) * tile_bytes + (kTileTokens + t % kTileTokens) * row_bytes +
@@ -567,24 +581,24 @@ __global__ void __launch_bounds__(kAttMaxWarps * 32, 1) attend_kernel(KvView kv,
         __syncwarp();
       }
 
-      // ---- scores: [heads] x [16 TT tokens]
-      float c[2 * TT][4];
+      // ---- scores: [16 TT tokens] x [heads]; rows g and g + 8 of each tile, columns j2 and j2 + 1
+      float c[TT][NT][4];
 #pragma unroll
       for (int t = 0; t < TT; ++t) {
         const uint32_t k32 = st32 + t * tile_bytes + k_row;
-        float(&c0)[4] = c[2 * t], (&c1)[4] = c[2 * t + 1];
-        float d0[4] = {}, d1[4] = {};  // a second sum: kE4m3's lo; kBf16's and kF16's odd blocks (a shorter chain)
-        int i0[4] = {}, i1[4] = {}, r0[4] = {}, r1[4] = {};
-        c0[0] = c0[1] = c0[2] = c0[3] = c1[0] = c1[1] = c1[2] = c1[3] = 0.f;
+        float d[NT][4] = {};  // a second sum for the odd blocks: a shorter chain
+        int ci[3][NT][4] = {};
+#pragma unroll
+        for (int h = 0; h < NT; ++h) c[t][h][0] = c[t][h][1] = c[t][h][2] = c[t][h][3] = 0.f;
         if (FORM == kBf16) {
 #pragma unroll
           for (int b = 0; b < NB; ++b) {
             if (ANY && b >= nb) continue;
             uint32_t k[4];
             ldsm4(k, k32 + (((2 * b + k_c) ^ sw) << 4));
-            const uint32_t *q = qa + b * 2 * HALVES;
-            mma16816(b & 1 ? d0 : c0, q[0], q[HALVES - 1], q[HALVES], q[2 * HALVES - 1], k[0], k[1]);
-            mma16816(b & 1 ? d1 : c1, q[0], q[HALVES - 1], q[HALVES], q[2 * HALVES - 1], k[2], k[3]);
+#pragma unroll
+            for (int h = 0; h < NT; ++h)
+              mma16816(b & 1 ? d[h] : c[t][h], k[0], k[1], k[2], k[3], qa[h][2 * b], qa[h][2 * b + 1]);
           }
         } else {
 #pragma unroll
@@ -592,179 +606,165 @@ __global__ void __launch_bounds__(kAttMaxWarps * 32, 1) attend_kernel(KvView kv,
             if (ANY && 2 * p >= nb) continue;
             uint32_t w[4];  // (tokens 0-7 | 8-15) x (block 2p | 2p + 1)
             ldsm4(w, k32 + (((2 * p + k_c) ^ sw) << 4));
-            if ((ANY || (NB & 1)) && 2 * p + 1 >= nb) w[2] = w[3] = 0;  // (past the row's end: anything, NaN too)
-            if (FORM == kE4m3) {
-              const uint32_t *q = qa + p * 4 * HALVES;
-              mma_e4m3(c0, q[0], q[1], q[2], q[3], w[0], w[2]);
-              mma_e4m3(c1, q[0], q[1], q[2], q[3], w[1], w[3]);
-              if (WIDE) {
-                q += 4 * (HALVES - 1);
-                mma_e4m3(d0, q[0], q[1], q[2], q[3], w[0], w[2]);
-                mma_e4m3(d1, q[0], q[1], q[2], q[3], w[1], w[3]);
-              }
-            } else if (FORM == kInt8) {
-              const uint32_t *q = qa + p * 6;
-              mma_s8(i0, q[0], q[1], q[2], q[3], w[0], w[2]);
-              mma_s8(i1, q[0], q[1], q[2], q[3], w[1], w[3]);
-              mma_s8(r0, q[4], 0, q[5], 0, w[0], w[2]);
-              mma_s8(r1, q[4], 0, q[5], 0, w[1], w[3]);
+            if (FORM == kInt8) {  // (past the row's end q's terms are 0 and any code will do)
+#pragma unroll
+              for (int h = 0; h < NT; ++h)
+#pragma unroll
+                for (int k = 0; k < 3; ++k)
+                  mma_s8(ci[k][h], w[0], w[1], w[2], w[3], qa[h][p * 6 + 2 * k], qa[h][p * 6 + 2 * k + 1]);
             } else {
 #pragma unroll
               for (int x = 0; x < 2; ++x) {
                 const int b = 2 * p + x;
                 if (b >= NB || (ANY && b >= nb)) continue;
-                const uint32_t *q = qa + b * 4;
-                uint32_t even, odd;
-                codes_to_f16<TYPE>(w[2 * x], even, odd);
-                mma_f16(x ? d0 : c0, q[0], q[1], q[2], q[3], even, odd);
-                codes_to_f16<TYPE>(w[2 * x + 1], even, odd);
-                mma_f16(x ? d1 : c1, q[0], q[1], q[2], q[3], even, odd);
+                uint32_t k0, k1, k2, k3;
+                key_codes_to_f16<TYPE>(w[2 * x], k0, k2);
+                key_codes_to_f16<TYPE>(w[2 * x + 1], k1, k3);
+#pragma unroll
+                for (int h = 0; h < NT; ++h) mma_f16(x ? d[h] : c[t][h], k0, k1, k2, k3, qa[h][2 * b], qa[h][2 * b + 1]);
               }
             }
           }
         }
-#pragma unroll
-        for (int e = 0; e < (WIDE ? 4 : 2); ++e) {
-          if (FORM == kE4m3) {
-            c0[e] = fmaf(WIDE ? d0[e] : c0[(e + 2) & 3], 0.03125f, c0[e]);
-            c1[e] = fmaf(WIDE ? d1[e] : c1[(e + 2) & 3], 0.03125f, c1[e]);
-          } else if (FORM == kInt8) {
-            c0[e] = fmaf((float)(i0[e] * 128 + i0[(e + 2) & 3]), 128.f, (float)r0[e]);
-            c1[e] = fmaf((float)(i1[e] * 128 + i1[(e + 2) & 3]), 128.f, (float)r1[e]);
-          } else {
-            c0[e] += d0[e];
-            c1[e] += d1[e];
-          }
+        float ks[2] = {1.f, 1.f};
+        if (TYPE != LORA_KV_BF16) {
+          const uint8_t *sc = stp + t * tile_bytes + 2 * kTileTokens * row_bytes;
+          ks[0] = *reinterpret_cast<const float *>(sc + g * 4);
+          ks[1] = *reinterpret_cast<const float *>(sc + g * 4 + 32);
         }
+#pragma unroll
+        for (int h = 0; h < NT; ++h)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            if (FORM == kInt8)
+              c[t][h][e] = fmaf((float)(ci[0][h][e] * 128 + ci[1][h][e]), 128.f, (float)ci[2][h][e]);
+            else
+              c[t][h][e] += d[h][e];
+            c[t][h][e] *= TYPE == LORA_KV_BF16 ? qs[h][e & 1] : ks[e >> 1] * qs[h][e & 1];
+          }
       }
 
       // ---- weights
-      float vs[2 * TT][2];
+      float vs[TT][2];
+      if (TYPE != LORA_KV_BF16) {
 #pragma unroll
-      for (int n = 0; n < 2 * TT; ++n) {
-        const int t = n / 2, tok = (n & 1) * 8 + 2 * quad;  // of the tile
-        float2 ks = make_float2(a.scale2, a.scale2);
-        if (TYPE != LORA_KV_BF16) {
-          const uint8_t *sc = stp + t * tile_bytes + 2 * kTileTokens * row_bytes;
-          ks = *reinterpret_cast<const float2 *>(sc + tok * 4);
-          ks.x *= a.scale2;
-          ks.y *= a.scale2;
-          const float2 u = *reinterpret_cast<const float2 *>(sc + (kTileTokens + tok) * 4);
-          vs[n][0] = u.x;
-          vs[n][1] = u.y;
+        for (int t = 0; t < TT; ++t) {
+          const uint8_t *sc = stp + t * tile_bytes + 2 * kTileTokens * row_bytes + kTileTokens * 4;
+          vs[t][0] = *reinterpret_cast<const float *>(sc + g * 4);
+          vs[t][1] = *reinterpret_cast<const float *>(sc + g * 4 + 32);
         }
+      }
+      if (partial) {
 #pragma unroll
-        for (int h = 0; h < HALVES; ++h) {
-          c[n][2 * h] *= FORM == kBf16 ? ks.x : ks.x * qs[h];
-          c[n][2 * h + 1] *= FORM == kBf16 ? ks.y : ks.y * qs[h];
-        }
-        if (partial) {
-          const bool off = bad >> t & 1;
+        for (int t = 0; t < TT; ++t)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const int j = t * kTileTokens + tok + e;
-            if (j < lo || j >= hi || off) {
-              c[n][e] = c[n][2 + e] = -INFINITY;
-              if (TYPE != LORA_KV_BF16) vs[n][e] = 0.f;
+            const int j = t * kTileTokens + g + 8 * e;
+            if (j < lo || j >= hi || (bad >> t & 1)) {
+#pragma unroll
+              for (int h = 0; h < NT; ++h) c[t][h][2 * e] = c[t][h][2 * e + 1] = -INFINITY;
+              if (TYPE != LORA_KV_BF16) vs[t][e] = 0.f;
             }
           }
-        }
       }
-      float mx[HALVES], base_m[HALVES], fade = 1.f;
+      // m is a reference, within 2^kSlack of the running maximum: while no
+      // score passes it by more, nothing is exchanged and nothing rescaled.
+      // V's scales likewise have vtop, within 2^kVSlack of the largest so far.
+      float mx[NT][2], vm = 0.f;
       bool moved = false;
 #pragma unroll
-      for (int h = 0; h < HALVES; ++h) {
-        mx[h] = m[h];
+      for (int h = 0; h < NT; ++h)
 #pragma unroll
-        for (int n = 0; n < 2 * TT; ++n) mx[h] = fmaxf(mx[h], fmaxf(c[n][2 * h], c[n][2 * h + 1]));
-        mx[h] = fmaxf(mx[h], __shfl_xor_sync(~0u, mx[h], 1));
-        mx[h] = fmaxf(mx[h], __shfl_xor_sync(~0u, mx[h], 2));
-        base_m[h] = mx[h] == -INFINITY ? 0.f : mx[h];
-        moved |= mx[h] > m[h];
-      }
-      float unit = 0.f;
-      if (TYPE != LORA_KV_BF16) {
-        // The weights times V's scales become fp16 in units of 2^-15 of the
-        // largest scale so far: none overflows, and what is below 2^-29 of it
-        // still has its place.
-        float vm = vtop;
+        for (int e = 0; e < 2; ++e) {
+          mx[h][e] = c[0][h][e];
 #pragma unroll
-        for (int n = 0; n < 2 * TT; ++n) vm = fmaxf(vm, fmaxf(vs[n][0], vs[n][1]));
-        vm = fmaxf(vm, __shfl_xor_sync(~0u, vm, 1));
-        vm = fmaxf(vm, __shfl_xor_sync(~0u, vm, 2));
-        if (vm > vtop) {
-          fade = __fdividef(vtop, vm);
-          vtop = vm;
-          moved = true;
+          for (int t = 0; t < TT; ++t) mx[h][e] = fmaxf(mx[h][e], fmaxf(c[t][h][e], c[t][h][e + 2]));
+          moved |= mx[h][e] > m[h][e] + kSlack;
         }
-        unit = vtop > 0.f ? 0x1p15f / vtop : 0.f;
+      if (TYPE != LORA_KV_BF16) {
+#pragma unroll
+        for (int t = 0; t < TT; ++t) vm = fmaxf(vm, fmaxf(vs[t][0], vs[t][1]));
+        moved |= vm > vtop * (1 << kVSlack);
       }
       if (__any_sync(~0u, moved)) {
+        float fade = 1.f;
+        if (TYPE != LORA_KV_BF16) {
+          vm = fmaxf(vm, __shfl_xor_sync(~0u, vm, 4));
+          vm = fmaxf(vm, __shfl_xor_sync(~0u, vm, 8));
+          vm = fmaxf(vm, __shfl_xor_sync(~0u, vm, 16));
+          if (vm > vtop) {
+            fade = __fdividef(vtop, vm);
+            vtop = vm;
+            unit = exp2_int(15 - kSlack - kVSlack) / vtop;
+          }
+        }
 #pragma unroll
-        for (int h = 0; h < HALVES; ++h) {
-          float alpha = exp2_fast(m[h] - base_m[h]);
-          l[h] *= alpha;
-          m[h] = mx[h];
-          alpha *= fade;
+        for (int h = 0; h < NT; ++h)
 #pragma unroll
-          for (int n = 0; n < 2 * NB; ++n) {
-            if (ANY && n >= 2 * nb) continue;
-            o[n][2 * h] *= alpha;
-            o[n][2 * h + 1] *= alpha;
-            if (!WIDE) {
-              o[n][2] *= alpha;
-              o[n][3] *= alpha;
+          for (int e = 0; e < 2; ++e) {
+            float x = mx[h][e];
+            x = fmaxf(x, __shfl_xor_sync(~0u, x, 4));
+            x = fmaxf(x, __shfl_xor_sync(~0u, x, 8));
+            x = fmaxf(x, __shfl_xor_sync(~0u, x, 16));
+            x = fmaxf(x, m[h][e]);
+            float alpha = exp2_fast(m[h][e] - (x == -INFINITY ? 0.f : x));
+            l[h][e] *= alpha;
+            m[h][e] = x;
+            alpha *= fade;
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+              if (ANY && b >= nb) continue;
+              o[h][b][e] *= alpha;
+              o[h][b][e + 2] *= alpha;
             }
           }
-        }
       }
-      // as two terms: hi keeps the leading bits of the type (cut, so that the rest is exact), lo the rest's
-      uint32_t ph[2 * TT][HALVES], pl[2 * TT][HALVES];
+      // The weights times V's scales become fp16 in units such that none
+      // overflows (2^9 over vtop); what is below 2^-33 of the largest is lost.
+      // As two terms: hi keeps the type's leading bits (cut, so that the rest is
+      // exact), lo the rest's.  Each turned: a thread then has two tokens of head g.
+      uint32_t ph[TT][NT][2], pl[TT][NT][2];
 #pragma unroll
-      for (int n = 0; n < 2 * TT; ++n)
+      for (int h = 0; h < NT; ++h) {
+        const float base[2] = {m[h][0] == -INFINITY ? 0.f : m[h][0], m[h][1] == -INFINITY ? 0.f : m[h][1]};
 #pragma unroll
-        for (int h = 0; h < HALVES; ++h) {
-          float p0 = exp2_fast(c[n][2 * h] - base_m[h]), p1 = exp2_fast(c[n][2 * h + 1] - base_m[h]);
-          l[h] += p0 + p1;
-          if (TYPE == LORA_KV_BF16) {
-            ph[n][h] = __byte_perm(__float_as_uint(p0), __float_as_uint(p1), 0x7632);
-            pl[n][h] = pack_bf16x2(p0 - bf16_lo(ph[n][h]), p1 - bf16_hi(ph[n][h]));
-          } else {
-            p0 *= vs[n][0] * unit;
-            p1 *= vs[n][1] * unit;
-            const float h0 = __uint_as_float(__float_as_uint(p0) & 0xffffe000u);
-            const float h1 = __uint_as_float(__float_as_uint(p1) & 0xffffe000u);
-            ph[n][h] = pack_f16x2(h0, h1);
-            pl[n][h] = pack_f16x2(p0 - h0, p1 - h1);
+        for (int t = 0; t < TT; ++t)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {  // tokens g and g + 8
+            float p0 = exp2_fast(c[t][h][2 * e] - base[0]), p1 = exp2_fast(c[t][h][2 * e + 1] - base[1]);
+            l[h][0] += p0;
+            l[h][1] += p1;
+            if (TYPE == LORA_KV_BF16) {
+              const uint32_t hi2 = __byte_perm(__float_as_uint(p0), __float_as_uint(p1), 0x7632);
+              ph[t][h][e] = turn(hi2);
+              pl[t][h][e] = turn(pack_bf16x2(p0 - bf16_lo(hi2), p1 - bf16_hi(hi2)));
+            } else {
+              const float w = vs[t][e] * unit;
+              p0 *= w;
+              p1 *= w;
+              const float h0 = __uint_as_float(__float_as_uint(p0) & 0xffffe000u);
+              const float h1 = __uint_as_float(__float_as_uint(p1) & 0xffffe000u);
+              ph[t][h][e] = turn(pack_f16x2(h0, h1));
+              pl[t][h][e] = turn(pack_f16x2(p0 - h0, p1 - h1));
+            }
           }
-        }
+      }
 
-      // ---- weighted values
+      // ---- weighted values: [16 dims] x [heads]
 #pragma unroll
       for (int t = 0; t < TT; ++t) {
         const uint32_t v32 = st32 + t * tile_bytes + v_row;
-        auto add = [&](float(&acc)[4], uint32_t b0, uint32_t b1) {
-          auto mma = [&](uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
-            if (TYPE == LORA_KV_BF16)
-              mma16816(acc, a0, a1, a2, a3, b0, b1);
-            else
-              mma_f16(acc, a0, a1, a2, a3, b0, b1);
-          };
-          if (WIDE) {
-            mma(ph[2 * t][0], ph[2 * t][HALVES - 1], ph[2 * t + 1][0], ph[2 * t + 1][HALVES - 1]);
-            mma(pl[2 * t][0], pl[2 * t][HALVES - 1], pl[2 * t + 1][0], pl[2 * t + 1][HALVES - 1]);
-          } else {
-            mma(ph[2 * t][0], pl[2 * t][0], ph[2 * t + 1][0], pl[2 * t + 1][0]);
-          }
-        };
         if (TYPE == LORA_KV_BF16) {
 #pragma unroll
           for (int b = 0; b < NB; ++b) {
             if (ANY && b >= nb) continue;
             uint32_t v[4];
             ldsm4t(v, v32 + (((2 * b + v_c) ^ sw) << 4));
-            add(o[2 * b], v[0], v[1]);
-            add(o[2 * b + 1], v[2], v[3]);
+#pragma unroll
+            for (int h = 0; h < NT; ++h) {
+              mma16816(o[h][b], v[0], v[1], v[2], v[3], ph[t][h][0], ph[t][h][1]);
+              mma16816(o[h][b], v[0], v[1], v[2], v[3], pl[t][h][0], pl[t][h][1]);
+            }
           }
         } else {
 #pragma unroll
@@ -776,11 +776,14 @@ __global__ void __launch_bounds__(kAttMaxWarps * 32, 1) attend_kernel(KvView kv,
             for (int x = 0; x < 2; ++x) {
               const int b = 2 * p + x;
               if (b >= NB || (ANY && b >= nb)) continue;
-              uint32_t e0, o0, e1, o1;
-              codes_to_f16<TYPE>(w[2 * x], e0, o0);
-              codes_to_f16<TYPE>(w[2 * x + 1], e1, o1);
-              add(o[2 * b], e0, e1);
-              add(o[2 * b + 1], o0, o1);
+              uint32_t v0, v1, v2, v3;  // even and odd dims of tokens 0-7, then of 8-15
+              codes_to_f16<TYPE>(w[2 * x], v0, v1);
+              codes_to_f16<TYPE>(w[2 * x + 1], v2, v3);
+#pragma unroll
+              for (int h = 0; h < NT; ++h) {
+                mma_f16(o[h][b], v0, v1, v2, v3, ph[t][h][0], ph[t][h][1]);
+                mma_f16(o[h][b], v0, v1, v2, v3, pl[t][h][0], pl[t][h][1]);
+              }
             }
           }
         }
@@ -976,21 +979,21 @@ using AttendKernel = void (*)(KvView, KvSeqs, AttendArgs);
 // of a step (a wait, the running maximum) is spread over as many bytes.
 struct Variant {
   AttendKernel kernel[2];  // up to 8 query heads per key head, more
-  int tt;
+  int tt, warps;
 };
 
-template <int TYPE, int DIM, bool ANY, int TT>
+template <int TYPE, int DIM, bool ANY, int TT, int WARPS>
 Variant variant() {
-  return {{attend_kernel<TYPE, DIM, ANY, TT, false>, attend_kernel<TYPE, DIM, ANY, TT, true>}, TT};
+  return {{attend_kernel<TYPE, DIM, ANY, TT, WARPS, 1>, attend_kernel<TYPE, DIM, ANY, TT, WARPS, 2>}, TT, WARPS};
 }
 
 template <int TYPE>
 Variant variant_of(int dim) {
-  constexpr int W = TYPE == LORA_KV_BF16 ? 1 : 2;
-  if (dim == 64) return variant<TYPE, 64, false, 2 * W>();
-  if (dim == 128) return variant<TYPE, 128, false, W>();
-  if (dim == 256) return variant<TYPE, 256, false, 1>();
-  return dim < 128 ? variant<TYPE, 128, true, W>() : variant<TYPE, 256, true, 1>();
+  constexpr int W = TYPE == LORA_KV_BF16 ? 1 : 2, N = TYPE == LORA_KV_BF16 ? 8 : 12;
+  if (dim == 64) return variant<TYPE, 64, false, 2 * W, N>();
+  if (dim == 128) return variant<TYPE, 128, false, W, N>();
+  if (dim == 256) return variant<TYPE, 256, false, 1, 8>();
+  return dim < 128 ? variant<TYPE, 128, true, W, N>() : variant<TYPE, 256, true, 1, 8>();
 }
 Variant variant_of(int type, int dim) {
   return type == LORA_KV_BF16   ? variant_of<LORA_KV_BF16>(dim)
@@ -998,22 +1001,22 @@ Variant variant_of(int type, int dim) {
                                 : variant_of<LORA_KV_INT8>(dim);
 }
 
-constexpr int kAttStatic = 2560;  // at least what the kernel's static shared memory takes
+constexpr int kAttStatic = 3584;  // at least what the kernel's static shared memory takes
 
-// Warps and stages: at least 3 stages a warp, 8 warps where that fits; the
-// warps' first pieces (state_bytes each) stay in shared memory where that costs
-// no warp.
+// Warps and stages: the most warps that leave each 3 stages (2 with more than
+// 8 warps); their first pieces (state_bytes each) stay in shared memory where
+// that costs no warp.
 struct Geometry {
   int warps, stages, first;  // first: its offset in dynamic shared memory (0: in the workspace)
   int smem;
 };
-Geometry geometry(int stage_bytes, int state_bytes) {
-  const int room = kAttSmem - kAttStatic;
+Geometry geometry(int most, int stage_bytes, int state_bytes) {
+  const int room = kAttSmem - kAttStatic, least = most > 8 ? 2 : 3;
   Geometry g;
-  g.warps = room / (3 * stage_bytes);
-  g.warps = g.warps > kAttMaxWarps ? kAttMaxWarps : g.warps;
+  g.warps = room / (least * stage_bytes);
+  g.warps = g.warps > most ? most : g.warps;
   const int keep = g.warps * state_bytes;
-  const bool fits = room - keep >= 3 * stage_bytes * g.warps;
+  const bool fits = room - keep >= least * stage_bytes * g.warps;
   g.stages = (room - (fits ? keep : 0)) / (g.warps * stage_bytes);
   g.stages = g.stages > kAttMaxStages ? kAttMaxStages : g.stages;
   g.first = fits ? g.warps * g.stages * stage_bytes : 0;
@@ -1059,7 +1062,7 @@ int launch_attend(const lora_kv *kv, int layer, const KvSeqs &s, const AttendCal
   a.scale2 = c.scale * 1.44269504f;
   a.window = c.window;
   const size_t floats = state_floats(a.rows, kv->dim);
-  const Geometry g = geometry(v.tt * kv_tile_bytes(kv->type, kv->dim), int(floats * 4));
+  const Geometry g = geometry(v.warps, v.tt * kv_tile_bytes(kv->type, kv->dim), int(floats * 4));
   a.n_stages = g.stages;
   a.first_in_smem = g.first;
   uint8_t *ws = static_cast<uint8_t *>(c.ws);
