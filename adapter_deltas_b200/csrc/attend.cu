@@ -11,12 +11,14 @@
 //
 // Bound by HBM: 4 flops per cached element and query head, at most 16 query
 // heads to a byte.  So the split is by bytes, evenly, whatever the lengths:
-//  - The batch is one flat list of steps, ordered by (sequence, unit, step).  A
+//  - The batch is one flat list of slots, ordered by (sequence, unit, step).  A
 //    unit is one key head with up to 8 (or 16) of its query heads; a step is 16
-//    TT consecutive tokens of it.  Each block takes an equal range of the list
-//    (one block per SM), each of its warps an equal range of the block's.  Every
-//    block finds its place itself from the lengths (one scan), so there is no
-//    plan to keep and nothing of it is read on the host.
+//    TT consecutive tokens of it.  A unit has one slot for each step and one
+//    before them for what it costs to begin and end one (about a step's time).
+//    Each block takes an equal range of the list (one block per SM), each of its
+//    warps an equal range of the block's.  Every block finds its place itself from
+//    the lengths (one scan), so there is no plan to keep and nothing of it is read
+//    on the host.
 //  - A warp is on its own: one lane fetches its steps' tiles with bulk copies
 //    (one per 16 tokens: a tile is contiguous in the cache, K, V and scales)
 //    into the warp's ring of stages, several steps ahead, through the page
@@ -174,17 +176,19 @@ __host__ __device__ constexpr int q_regs(int form, int nb, int nt) {  // per n-t
   return nt * (form == kInt8 ? (nb + 1) / 2 * 6 : nb * 2);
 }
 
-// Length of sequence s where it is one that is attended to, else 0 (none, empty, in error).
-__device__ __forceinline__ int seq_len(const KvView &kv, const KvSeqs &s, int i) {
-  const int len = __ldg(s.lens + i);
+// A length that is attended to, else 0 (none, empty, in error).
+__device__ __forceinline__ int valid_len(const KvView &kv, const KvSeqs &s, int len) {
   return len > 0 && len <= ((long long)s.max_pages << kv.log2_page) ? len : 0;
 }
+__device__ __forceinline__ int seq_len(const KvView &kv, const KvSeqs &s, int i) {
+  return valid_len(kv, s, __ldg(s.lens + i));
+}
 __device__ __forceinline__ int first_token(int len, int window) { return window && len > window ? len - window : 0; }
-// Steps of a unit of a sequence, of tt tiles each and aligned to that: from the
-// first token's to the last one's.
-__device__ __forceinline__ int seq_steps(int len, int window, int tt) {
+// Slots of a unit of a sequence: one, and one for each step of tt tiles (aligned
+// to that) from the first token's to the last one's.  None without a token.
+__device__ __forceinline__ int unit_slots(int len, int window, int tt) {
   const int per = kTileTokens * tt;
-  return (len + per - 1) / per - first_token(len, window) / per;
+  return len ? (len + per - 1) / per - first_token(len, window) / per + 1 : 0;
 }
 
 // Write row r's result from its state: o = sums for 4 dims, m and l over all tokens.
@@ -207,7 +211,7 @@ __device__ __forceinline__ Ends finish(const AttendArgs &a, int head, float m, f
 
 // ------------------------------------------------------------------ kernel
 
-// What a stage of a ring holds (written for the first step of a unit or range).
+// What a stage of a ring holds (written for the first step of a unit or of a warp's range).
 struct Step {
   int seq, unit, pos, len;  // sequence, unit, first token of the step, tokens of the sequence
 };
@@ -227,7 +231,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(KvView kv, KvSeqs
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint64_t full[kAttMaxWarps][kAttMaxStages];
   __shared__ Step held[kAttMaxWarps][kAttMaxStages];
-  __shared__ long long scan[kAttMaxWarps], from[kAttMaxWarps];  // from: a warp's first step, from its sequence's first
+  __shared__ long long scan[kAttMaxWarps], from[kAttMaxWarps];  // from: a warp's first slot, from its sequence's first
   __shared__ int2 start[kAttMaxWarps];                          // {sequence, length} of it
   __shared__ int4 piece[2 * kAttMaxWarps];  // [2 warp + which]: {sequence (-1: none), unit, cut before 1 / after 2, -}
   __shared__ const float *where[2 * kAttMaxWarps];
@@ -249,7 +253,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(KvView kv, KvSeqs
   const int per = (s.n + blockDim.x - 1) / blockDim.x;
   const int s0 = min(s.n, tid * per), s1 = min(s.n, s0 + per);
   long long mine = 0;
-  for (int i = s0; i < s1; ++i) mine += seq_steps(seq_len(kv, s, i), a.window, TT);
+  for (int i = s0; i < s1; ++i) mine += unit_slots(seq_len(kv, s, i), a.window, TT);
   long long before = mine;  // inclusive scan over the block
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
@@ -266,29 +270,30 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(KvView kv, KvSeqs
       total += scan[i];
     }
   before -= mine;
-  // (no more blocks than steps: the join counts on every block in a row having a part)
-  const unsigned long long steps_all = (unsigned long long)total * a.units;
-  const unsigned blocks = (unsigned)min((unsigned long long)gridDim.x, steps_all);
-  unsigned long long each = 0;  // steps of a block; the first `more` have one more
+  // (two slots at least to a block, so that it has a step: the join counts on
+  // every block in a row having a part)
+  const unsigned long long slots_all = (unsigned long long)total * a.units;
+  const unsigned blocks = (unsigned)min((unsigned long long)gridDim.x, slots_all / 2);
+  unsigned long long each = 0;  // slots of a block; the first `more` have one more
   unsigned more = 0;
-  if (steps_all >> 32)
-    each = steps_all / max(blocks, 1u);
+  if (slots_all >> 32)
+    each = slots_all / max(blocks, 1u);
   else
-    each = (unsigned)steps_all / max(blocks, 1u);
-  more = (unsigned)(steps_all - each * blocks);
+    each = (unsigned)slots_all / max(blocks, 1u);
+  more = (unsigned)(slots_all - each * blocks);
   const long long b0 = each * blockIdx.x + min(blockIdx.x, more);
-  const int steps = blockIdx.x < blocks ? (int)each + (blockIdx.x < more) : 0;
-  const int wq = steps / n_warps, wr = steps - wq * n_warps;
+  const int slots = blockIdx.x < blocks ? (int)each + (blockIdx.x < more) : 0;
+  const int wq = slots / n_warps, wr = slots - wq * n_warps;
   if (mine > 0) {  // whose range starts in this thread's sequences
     const long long lo = before * a.units - b0, hi = lo + mine * a.units;
-    if (lo < steps && hi > 0) {
+    if (lo < slots && hi > 0) {
       for (int w = 0; w < n_warps; ++w) {
         const int at = wq * w + min(w, wr);
-        if (at < lo || at >= hi || at >= steps) continue;
+        if (at < lo || at >= hi || at >= slots) continue;
         long long p = lo;
         for (int i = s0; i < s1; ++i) {
           const int len = seq_len(kv, s, i);
-          const long long e = p + (long long)seq_steps(len, a.window, TT) * a.units;
+          const long long e = p + (long long)unit_slots(len, a.window, TT) * a.units;
           if (at < e) {
             start[w] = make_int2(i, len);
             from[w] = at - p;
@@ -300,16 +305,19 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(KvView kv, KvSeqs
     }
   }
   __syncthreads();
-  const int count = wq + (warp < wr);  // this warp's steps
+  const int count = wq + (warp < wr);  // this warp's slots
 
   uint8_t *ring = smem + (size_t)warp * a.n_stages * stage_bytes;
   if (count > 0) {
     // ---- fetching side: the next step to fetch, and pages of up to 32 tiles
-    int left = count;  // steps not yet fetched
+    int left = count;  // slots not yet passed
+    int fetched = 0;   // steps fetched or being so
     int fseq = start[warp].x, flen = start[warp].y;
     int funit, fpos;   // fpos: first token of the step
+    bool fnew = true;  // the step to fetch is the first of a unit or of the range
+    bool own_slot;     // the unit's own slot is to be passed first
     {
-      const int n = seq_steps(flen, a.window, TT);
+      const int n = unit_slots(flen, a.window, TT);
       const unsigned long long off = from[warp];
       int step;
       if (off >> 32) {
@@ -319,62 +327,87 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(KvView kv, KvSeqs
         funit = (int)((unsigned)off / (unsigned)n);
         step = (int)((unsigned)off - (unsigned)funit * n);
       }
-      fpos = (first_token(flen, a.window) / kStep + step) * kStep;
+      own_slot = step == 0;
+      fpos = (first_token(flen, a.window) / kStep + max(step - 1, 0)) * kStep;
     }
     const bool starts_inside = fpos > first_token(flen, a.window);  // of its unit
-    bool fnew = true;             // the step to fetch is the first of a unit or of the range
-    int pages = 0, pbase = -1;    // lane j: page of the sequence's tile pbase + j
-    unsigned bad_tiles = 0;       // bits stage * TT ..: tiles of a stage that are on no page of the cache
+    unsigned bad_tiles = 0;     // bits stage * TT ..: tiles of a stage that are on no page of the cache
     const long long head_stride = kv_head_stride(kv);
     const uint8_t *fhead = kv.base + (funit / a.head_groups) * head_stride;
     // a step's tiles lie in one page, one behind the other, unless pages are shorter
     const bool one_copy = TT == 1 || (1 << kv.log2_page) >= kStep;
+    // lane i: page of the sequence's tile base + i, or -1
+    auto load_pages = [&](int seq, int len, int base) {
+      const int tok = (base + lane) * kTileTokens;
+      return tok < len ? __ldg(s.table + (long long)seq * s.max_pages + (tok >> kv.log2_page)) : -1;
+    };
+    int pbase = fpos / kTileTokens & ~31, pages = load_pages(fseq, flen, pbase);
+    // the sequence after: its length is read when this one begins, its first pages when this one's last unit does
+    int nlen = fseq + 1 < s.n ? __ldg(s.lens + fseq + 1) : 0, npages = 0;
+    auto load_next = [&]() {
+      if (funit != a.units - 1 || fseq + 1 >= s.n) return;
+      nlen = valid_len(kv, s, nlen);
+      npages = load_pages(fseq + 1, nlen, first_token(nlen, a.window) / kStep * TT & ~31);
+    };
+    load_next();
 
     auto fetch = [&](int stage) {
+      if (own_slot) {
+        --left;
+        own_slot = false;
+      }
       if (left <= 0) return;
       --left;
-      const int t = fpos / kTileTokens, want = t & ~31;
-      if (want != pbase) {
-        pbase = want;
-        pages = -1;
-        if ((pbase + lane) * kTileTokens < flen)
-          pages = __ldg(s.table + (long long)fseq * s.max_pages + (((pbase + lane) * kTileTokens) >> kv.log2_page));
+      ++fetched;
+      const int t = fpos / kTileTokens;
+      if ((t & ~31) != pbase) {
+        pbase = t & ~31;
+        pages = load_pages(fseq, flen, pbase);
       }
-      // tiles [t0, t1) of the step: lane i has tile i (or lane 0 all of them)
+      // tiles [t0, t1) of the step, by lane 0 in one copy or by a lane each
       const int t0 = max(first_token(flen, a.window) / kTileTokens - t, 0);
       const int t1 = min((flen - fpos + kTileTokens - 1) / kTileTokens, TT);
-      const int mine = one_copy ? t0 : t0 + lane;
-      const int page = __shfl_sync(~0u, pages, (t + mine) & 31);
-      const long long at = kv_tile_offset(kv, page, fpos + mine * kTileTokens);
-      const unsigned ok = __ballot_sync(~0u, at >= 0 && lane < (one_copy ? 1 : t1 - t0));
-      const int n = one_copy ? (ok ? t1 - t0 : 0) : __popc(ok);
+      const int tile = one_copy ? t0 : t0 + lane;
+      const int page = __shfl_sync(~0u, pages, (t + tile) & 31);
+      const long long at = kv_tile_offset(kv, page, fpos + tile * kTileTokens);
+      bool copy = at >= 0 && lane < (one_copy ? 1 : t1 - t0);
+      int n = at >= 0 ? t1 - t0 : 0;
+      if (TT > 1 && !one_copy) n = __popc(__ballot_sync(~0u, copy));
       if (lane == 0) {
         if (fnew) held[warp][stage] = {fseq, funit, fpos, flen};
         mbar_arrive_expect_tx(&full[warp][stage], n * tile_bytes);
       }
       if (n < t1 - t0) {
-        bad_tiles |= (((1u << t1) - (1u << t0)) & ~(one_copy ? 0u : ok << t0)) << (stage * TT);
+        const unsigned ok = TT > 1 && !one_copy ? __ballot_sync(~0u, copy) << t0 : 0u;
+        bad_tiles |= (((1u << t1) - (1u << t0)) & ~ok) << (stage * TT);
         if (lane == 0) set_status(kv.status, LORA_ERR_BAD_ID);
       }
       __syncwarp();
-      if (ok >> lane & 1)
-        bulk_g2s(ring + stage * stage_bytes + mine * tile_bytes, fhead + at, one_copy ? n * tile_bytes : tile_bytes,
+      if (copy)
+        bulk_g2s(ring + stage * stage_bytes + tile * tile_bytes, fhead + at, one_copy ? n * tile_bytes : tile_bytes,
                  &full[warp][stage]);
       fpos += kStep;
       fnew = fpos >= flen;
       if (fnew) {
+        own_slot = true;
         if (++funit == a.units) {
           funit = 0;
-          pbase = -1;
-          if (left > 0) {
-            do {
+          if (left > 1) {  // (another step is to come)
+            ++fseq;
+            flen = valid_len(kv, s, nlen);
+            pages = npages;
+            pbase = first_token(flen, a.window) / kStep * TT & ~31;
+            while (flen == 0) {
               ++fseq;
               flen = seq_len(kv, s, fseq);
-            } while (flen == 0);
+              pbase = -1;
+            }
+            nlen = fseq + 1 < s.n ? __ldg(s.lens + fseq + 1) : 0;
           }
         }
         fpos = first_token(flen, a.window) / kStep * kStep;
         fhead = kv.base + (funit / a.head_groups) * head_stride;
+        load_next();
       }
     };
 
@@ -465,7 +498,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(KvView kv, KvSeqs
       fetch(fstage);
       if (++fstage == a.n_stages) fstage = 0;
       if (i < 0) continue;
-      const bool end = i == count;
+      const bool end = i == fetched;
       if (end || cnew) {
         if (cseq >= 0) {
           // The unit's state leaves the registers: as its result when the warp
@@ -553,6 +586,13 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(KvView kv, KvSeqs
         }
         vtop = unit = 0.f;
         load_q();
+        {  // the next unit's q, towards this SM
+          const bool same = cunit + 1 < a.units;
+          const int nu = same ? cunit + 1 : 0, ns = cseq + !same, bytes = a.rows * dim * 2;
+          const uint8_t *q = a.q + ns * a.ldq + ((nu / a.head_groups) * a.group + (nu % a.head_groups) * ROWS) * (long long)dim * 2;
+          if (ns < s.n)
+            for (int x = lane * 128; x < bytes; x += 32 * 128) asm volatile("prefetch.global.L1 [%0];" ::"l"(q + x));
+        }
       }
       if (!mbar_wait_bounded(&full[warp][stage], phase, kv.status)) {
         // copies in flight must land before the block ends (again a bounded wait)
@@ -821,8 +861,8 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(KvView kv, KvSeqs
     if (!there || broken || !(tail_cut & 2) || (head_cut & 1)) {
       cut.x = -1;
     } else {
-      const unsigned long long step = b0 + steps + tail_steps - 1, big = (each + 1) * more;
-      cut.z = (int)(step < big ? step / (each + 1) : more + (step - big) / each);
+      const unsigned long long slot = b0 + slots + tail_steps - 1, big = (each + 1) * more;
+      cut.z = (int)(slot < big ? slot / (each + 1) : more + (slot - big) / each);
     }
     if (lane == 0) a.cut[blockIdx.x] = cut;
   }
@@ -830,44 +870,42 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(KvView kv, KvSeqs
     a.part[((size_t)blockIdx.x * 2 + tid / a.rows) * floats + a.rows + tid % a.rows] = -1.f;
   __syncthreads();
   const int quads = dim / 4;
-  for (int k = 0; k < n_runs; ++k) {
+  const int per_run = a.rows * quads;
+  for (int i0 = tid; i0 < n_runs * per_run && !broken; i0 += blockDim.x) {
+    const int k = i0 / per_run, r = (i0 - k * per_run) / quads, d = (i0 - k * per_run - r * quads) * 4;
     const int f = run[k], e = run[k + 1];
     const int4 p0 = piece[order[f]], p1 = piece[order[e - 1]];
     const bool whole = !(p0.z & 1) && !(p1.z & 2);
     const int kvh = p0.y / a.head_groups, h0 = (p0.y - kvh * a.head_groups) * ROWS;
-    if (broken) break;
-    for (int x = tid; x < a.rows * quads; x += blockDim.x) {
-      const int r = x / quads, d = (x - r * quads) * 4;
-      if (h0 + r >= a.group) break;
-      float mm = -INFINITY, ll = 0.f;
-      for (int i = f; i < e; ++i) mm = fmaxf(mm, where[order[i]][r]);
-      const float bm = mm == -INFINITY ? 0.f : mm;
-      float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (h0 + r >= a.group) continue;
+    float mm = -INFINITY, ll = 0.f;
+    for (int i = f; i < e; ++i) mm = fmaxf(mm, where[order[i]][r]);
+    const float bm = mm == -INFINITY ? 0.f : mm;
+    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 2
-      for (int i = f; i < e; ++i) {
-        const float *st = where[order[i]];
-        const float w = exp2_fast(st[r] - bm);
-        const float4 z = *reinterpret_cast<const float4 *>(st + state_head(a.rows) + r * dim + d);
-        ll = fmaf(w, st[a.rows + r], ll);
-        y.x = fmaf(w, z.x, y.x);
-        y.y = fmaf(w, z.y, y.y);
-        y.z = fmaf(w, z.z, y.z);
-        y.w = fmaf(w, z.w, y.w);
+    for (int i = f; i < e; ++i) {
+      const float *st = where[order[i]];
+      const float w = exp2_fast(st[r] - bm);
+      const float4 z = *reinterpret_cast<const float4 *>(st + state_head(a.rows) + r * dim + d);
+      ll = fmaf(w, st[a.rows + r], ll);
+      y.x = fmaf(w, z.x, y.x);
+      y.y = fmaf(w, z.y, y.y);
+      y.z = fmaf(w, z.z, y.z);
+      y.w = fmaf(w, z.w, y.w);
+    }
+    if (whole) {
+      const int hd = kvh * a.group + h0 + r;
+      const Ends fin = finish(a, hd, mm, ll);
+      if (a.lse && d == 0) a.lse[(long long)p0.x * a.n_heads + hd] = fin.lse;
+      *reinterpret_cast<uint2 *>(a.out + p0.x * a.ldo + ((long long)hd * dim + d) * 2) =
+          make_uint2(pack_bf16x2(y.x * fin.mul, y.y * fin.mul), pack_bf16x2(y.z * fin.mul, y.w * fin.mul));
+    } else {
+      float *st = a.part + ((size_t)blockIdx.x * 2 + (p0.z & 1 ? 0 : 1)) * floats;
+      if (d == 0) {
+        st[r] = mm;
+        st[a.rows + r] = ll;
       }
-      if (whole) {
-        const int hd = kvh * a.group + h0 + r;
-        const Ends fin = finish(a, hd, mm, ll);
-        if (a.lse && d == 0) a.lse[(long long)p0.x * a.n_heads + hd] = fin.lse;
-        *reinterpret_cast<uint2 *>(a.out + p0.x * a.ldo + ((long long)hd * dim + d) * 2) =
-            make_uint2(pack_bf16x2(y.x * fin.mul, y.y * fin.mul), pack_bf16x2(y.z * fin.mul, y.w * fin.mul));
-      } else {
-        float *st = a.part + ((size_t)blockIdx.x * 2 + (p0.z & 1 ? 0 : 1)) * floats;
-        if (d == 0) {
-          st[r] = mm;
-          st[a.rows + r] = ll;
-        }
-        *reinterpret_cast<float4 *>(st + state_head(a.rows) + r * dim + d) = y;
-      }
+      *reinterpret_cast<float4 *>(st + state_head(a.rows) + r * dim + d) = y;
     }
   }
 
