@@ -7,19 +7,24 @@
 // kv.cuh), gather reads held rows back as bf16.  Both are one pass over their
 // bytes; what bounds them is HBM.
 //
-// Work split: a row of one head's K or V is handled by `lanes` neighbouring
-// threads (a power of two, 8 elements or 16 bytes of bf16 each), which reduce
-// its largest magnitude with shuffles and store 8 or 16 bytes each into the
-// token's tile.  A block takes `rows` consecutive rows of the batch (about four
-// vectors per thread); its warps first look up each row's sequence (a 32-way
-// search in row_offsets: two dependent reads up to 1024 sequences) and page.
+// Work split: a row of one head's K or V (a vector) is handled by `lanes`
+// neighbouring threads (a power of two), each with 16 bytes of the held row: 8
+// elements of bf16 or 16 in 8 bits, whose largest magnitude they reduce with
+// shuffles.  A block takes `rows` consecutive rows of the batch, so
+// many that the blocks are resident at once (its start, a chain of dependent
+// reads, is then paid once); a thread's loads of 64 bytes are in flight
+// together.  What bounds the 8-bit forms beside HBM is the instructions per
+// element, so addresses are kept per thread and stepped.  The block's warps look up the rows' sequences (a 32-way search in
+// row_offsets, two dependent reads up to 1024 sequences, where the row before is
+// not in the same one), then a thread a row its length and page; append reads
+// its first input rows, which do not depend on that, before.
 #include <new>
 
 #include "kv.cuh"
 
 namespace lora {
 
-constexpr int kRowThreads = 256;
+constexpr int kRowThreads = 256, kRowBlocks = 5;  // blocks resident on an SM
 constexpr int kMaxBlockRows = 64;
 
 // Sequence of row t (largest s with off[s] <= t, if t < off[s + 1]), by one warp; -1 if none.
@@ -46,18 +51,34 @@ __device__ __forceinline__ int find_seq(const int32_t *off, int n, int t) {
 __device__ __forceinline__ void locate_rows(const KvView &kv, const KvSeqs &s, int first, int rows, long long *tile,
                                             int *tok) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int i = warp; i < rows; i += kRowThreads / 32) {
+  if (s.offsets) {
+    int seq = -1, from = 0, to = 0;
+    for (int i = warp; i < rows; i += kRowThreads / 32) {
+      const int t = first + i;
+      if (t < from || t >= to) {
+        seq = find_seq(s.offsets, s.n, t);
+        from = to = 0;
+        if (seq >= 0) {
+          from = __ldg(s.offsets + seq);
+          to = __ldg(s.offsets + seq + 1);
+        }
+      }
+      if (lane == 0) {
+        tile[i] = seq >= 0 ? (long long)from << 32 | (unsigned)to : 0;
+        tok[i] = seq;
+      }
+    }
+    __syncthreads();
+  }
+  const int i = threadIdx.x;
+  if (i < rows) {
     const int t = first + i;
     int seq = t, back = 1, own = 1;  // the row's distance from its sequence's end; the sequence's rows
     if (s.offsets) {
-      seq = find_seq(s.offsets, s.n, t);
-      if (seq >= 0) {
-        const int end = __ldg(s.offsets + seq + 1);
-        back = end - t;
-        own = end - __ldg(s.offsets + seq);
-      }
+      seq = tok[i];
+      back = (int)tile[i] - t;
+      own = (int)tile[i] - (int)(tile[i] >> 32);
     }
-    if (lane) continue;
     long long at = -1;
     int row = 0;
     if (seq >= 0) {
@@ -90,108 +111,171 @@ struct RowArgs {
   uint8_t *k, *v;     // [T, ld] bf16: read (append) or written (gather)
   long long ldk, ldv; // bytes
   int T, rows;        // rows per block
-  int lanes;          // threads per vector (power of two >= dim / 8)
+  int lanes;          // threads per vector (power of two >= dim / vec_elements)
+};
+__host__ __device__ constexpr int vec_elements(int type) { return 16 / kv_elt(type); }  // of a thread: 16 held bytes
+
+// The vectors of a block are numbered (row, K or V, head), heads fastest, as the
+// rows lie in memory; a thread takes every `step`-th.
+struct RowWalk {
+  int head, x;           // x = 2 * row + which
+  int by_head, by_x;     // step, as heads and x
+  __device__ RowWalk(int w, int step, int heads) {
+    x = w / heads;
+    head = w - x * heads;
+    by_x = step / heads;
+    by_head = step - by_x * heads;
+  }
+  __device__ void next(int heads) {
+    head += by_head;
+    x += by_x;
+    if (head >= heads) {
+      head -= heads;
+      ++x;
+    }
+  }
 };
 
-// Vector w of a block: (row, K or V, head), heads fastest, as the rows lie in memory.
-struct RowVec {
-  int row, which, head;
+// A thread's place in the held rows: the 16-byte chunk that starts with element e of a vector.
+template <int TYPE>
+struct HeldPlace {
+  int chunk;         // its bytes from the row's start
+  int shift, mask;   // of kv_chunk: chunk ^ (token >> shift & mask)
+  int row_bytes, head_stride;  // (a page is under 2 GiB)
+  __device__ HeldPlace(const KvView &kv, int e) {
+    row_bytes = kv.dim * kv_elt(TYPE);
+    const int low = (row_bytes / 16) & -(row_bytes / 16);
+    chunk = e * kv_elt(TYPE);
+    mask = min(low, 8) - 1;
+    shift = 3 - __popc(mask);
+    head_stride = (int)kv_head_stride(kv);
+  }
+  __device__ uint4 *operator()(uint8_t *tile, int tok, int which, int head) const {
+    return reinterpret_cast<uint4 *>(tile + head * head_stride + (which * kTileTokens + tok) * row_bytes +
+                                     (chunk ^ (tok >> shift & mask) << 4));
+  }
+  __device__ float *scale(uint8_t *tile, int tok, int which, int head) const {
+    return reinterpret_cast<float *>(tile + head * head_stride + 2 * kTileTokens * row_bytes) + which * kTileTokens + tok;
+  }
 };
-__device__ __forceinline__ RowVec row_vec(int w, int heads) {
-  RowVec r;
-  r.head = w % heads;
-  const int x = w / heads;
-  r.which = x & 1;
-  r.row = x >> 1;
-  return r;
-}
 
 template <int TYPE>
-__device__ __forceinline__ uint8_t *held_at(const KvView &kv, long long tile, int tok, const RowVec &r, int e) {
-  constexpr int ES = kv_elt(TYPE);
-  const int row_bytes = kv.dim * ES, b = e * ES;
-  uint8_t *t = kv.base + tile + r.head * kv_head_stride(kv) + (r.which * kTileTokens + tok) * row_bytes;
-  return t + kv_chunk(b / 16, tok, row_bytes / 16) * 16 + b % 16;
-}
-__device__ __forceinline__ float *scale_at(const KvView &kv, long long tile, int tok, const RowVec &r) {
-  uint8_t *t = kv.base + tile + r.head * kv_head_stride(kv) + 2 * kTileTokens * kv.dim;
-  return reinterpret_cast<float *>(t) + r.which * kTileTokens + tok;
-}
-
-template <int TYPE>
-__global__ void __launch_bounds__(kRowThreads) kv_append_kernel(KvView kv, KvSeqs s, RowArgs a) {
+__global__ void __launch_bounds__(kRowThreads, kRowBlocks) kv_append_kernel(KvView kv, KvSeqs s, RowArgs a) {
+  constexpr int E = vec_elements(TYPE), U = E / 8, kAhead = 4 / U;
   __shared__ long long tile[kMaxBlockRows];
   __shared__ int tok[kMaxBlockRows];
+  const int first = blockIdx.x * a.rows, rows = min(a.rows, a.T - first);
+  const int part = threadIdx.x & (a.lanes - 1), e = part * E, step = kRowThreads / a.lanes;
+  const bool on = e < kv.dim;
+  const HeldPlace<TYPE> held(kv, e);
+  const uint8_t *src_k = a.k + first * a.ldk + e * 2, *src_v = a.v + first * a.ldv + e * 2;
+  RowWalk in(threadIdx.x / a.lanes, step, kv.heads), to = in;
+  const int turns = (rows * 2 * kv.heads + step * kAhead - 1) / (step * kAhead);
   griddep_wait();
   griddep_launch_dependents();
-  const int first = blockIdx.x * a.rows, rows = min(a.rows, a.T - first);
-  check_offsets(kv, s, a.T);
-  locate_rows(kv, s, first, rows, tile, tok);
-  __syncthreads();
-  const int part = threadIdx.x & (a.lanes - 1), e = part * 8;
-  const int n = rows * 2 * kv.heads;
-  // (whole groups of lanes leave the loop together, but a warp may not: the
-  // shuffles name the group's own lanes only)
-  const unsigned group = (a.lanes == 32 ? ~0u : ((1u << a.lanes) - 1u) << (threadIdx.x & 31 & ~(a.lanes - 1)));
-  for (int w = threadIdx.x / a.lanes; w < n; w += kRowThreads / a.lanes) {
-    const RowVec r = row_vec(w, kv.heads);
-    if (tile[r.row] < 0) continue;
-    uint4 u = make_uint4(0, 0, 0, 0);
-    if (e < kv.dim) {
-      const uint8_t *src = r.which ? a.v + (first + r.row) * a.ldv : a.k + (first + r.row) * a.ldk;
-      u = __ldg(reinterpret_cast<const uint4 *>(src + (r.head * kv.dim + e) * 2));
+  for (int turn = 0; turn < turns; ++turn) {  // (every thread takes every turn: the shuffles are the whole warp's)
+    uint4 u[kAhead][U];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+#pragma unroll
+      for (int k = 0; k < U; ++k) u[i][k] = make_uint4(0, 0, 0, 0);
+      if (on && in.x < 2 * rows) {
+        const int row = in.x >> 1;
+        const uint8_t *src = (in.x & 1 ? src_v + row * a.ldv : src_k + row * a.ldk) + in.head * kv.dim * 2;
+#pragma unroll
+        for (int k = 0; k < U; ++k) u[i][k] = __ldg(reinterpret_cast<const uint4 *>(src) + k);
+      }
+      in.next(kv.heads);
     }
-    if (TYPE == LORA_KV_BF16) {
-      if (e < kv.dim) *reinterpret_cast<uint4 *>(held_at<TYPE>(kv, tile[r.row], tok[r.row], r, e)) = u;
-    } else {
-      float x[8];
-      unpack8(u, x);
+    if (turn == 0) {
+      check_offsets(kv, s, a.T);
+      locate_rows(kv, s, first, rows, tile, tok);
+      __syncthreads();
+    }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int row = to.x >> 1, which = to.x & 1, head = to.head;
+      const long long at = row < rows ? tile[row] : -1;
+      to.next(kv.heads);
+      if (TYPE == LORA_KV_BF16) {
+        if (at >= 0 && on) *held(kv.base + at, tok[row], which, head) = u[i][0];
+        continue;
+      }
+      // the largest magnitude, as bits of bf16, two by two
       uint32_t m = 0;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) m = max(m, abs_bits(x[i]));
-      for (int d = a.lanes / 2; d; d >>= 1) m = max(m, __shfl_xor_sync(group, m, d));
-      const Quant q = quant_of<TYPE == LORA_KV_E4M3 ? 448 : 127>(__uint_as_float(m));
-      if (e < kv.dim)
-        *reinterpret_cast<uint2 *>(held_at<TYPE>(kv, tile[r.row], tok[r.row], r, e)) =
-            make_uint2(code4<TYPE>(x, q), code4<TYPE>(x + 4, q));
-      if (part == 0) *scale_at(kv, tile[r.row], tok[r.row], r) = q.scale;
+      for (int k = 0; k < U; ++k) {
+        const uint4 v = u[i][k];
+        m = __vmaxu2(m, __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu), __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu)));
+      }
+      for (int d = a.lanes / 2; d; d >>= 1) m = __vmaxu2(m, __shfl_xor_sync(~0u, m, d));
+      if (at < 0) continue;
+      const Quant q = quant_of<TYPE == LORA_KV_E4M3 ? 448 : 127>(__uint_as_float(max(m >> 16, m & 0xffffu) << 16));
+      uint32_t c[2 * U];
+#pragma unroll
+      for (int k = 0; k < U; ++k) {
+        float x[8];
+        unpack8(u[i][k], x);
+        c[2 * k] = code4<TYPE>(x, q);
+        c[2 * k + 1] = code4<TYPE>(x + 4, q);
+      }
+      if (on) *held(kv.base + at, tok[row], which, head) = make_uint4(c[0], c[1], c[2 * U - 2], c[2 * U - 1]);
+      if (part == 0) *held.scale(kv.base + at, tok[row], which, head) = q.scale;
     }
   }
 }
 
 template <int TYPE>
-__global__ void __launch_bounds__(kRowThreads) kv_gather_kernel(KvView kv, KvSeqs s, RowArgs a) {
+__global__ void __launch_bounds__(kRowThreads, kRowBlocks) kv_gather_kernel(KvView kv, KvSeqs s, RowArgs a) {
+  constexpr int E = vec_elements(TYPE), U = E / 8, kAhead = 4 / U;
   __shared__ long long tile[kMaxBlockRows];
   __shared__ int tok[kMaxBlockRows];
+  const int first = blockIdx.x * a.rows, rows = min(a.rows, a.T - first);
+  const int e = (threadIdx.x & (a.lanes - 1)) * E, step = kRowThreads / a.lanes;
+  const HeldPlace<TYPE> held(kv, e);
+  uint8_t *dst_k = a.k + first * a.ldk + e * 2, *dst_v = a.v + first * a.ldv + e * 2;
+  RowWalk from(threadIdx.x / a.lanes, step, kv.heads), to = from;
   griddep_wait();
   griddep_launch_dependents();
-  const int first = blockIdx.x * a.rows, rows = min(a.rows, a.T - first);
   check_offsets(kv, s, a.T);
   locate_rows(kv, s, first, rows, tile, tok);
   __syncthreads();
-  const int e = (threadIdx.x & (a.lanes - 1)) * 8;
-  const int n = rows * 2 * kv.heads;
   if (e >= kv.dim) return;
-  for (int w = threadIdx.x / a.lanes; w < n; w += kRowThreads / a.lanes) {
-    const RowVec r = row_vec(w, kv.heads);
-    if (tile[r.row] < 0) continue;
-    const uint8_t *src = held_at<TYPE>(kv, tile[r.row], tok[r.row], r, e);
-    uint4 u;
-    if (TYPE == LORA_KV_BF16) {
-      u = *reinterpret_cast<const uint4 *>(src);
-    } else {
-      const uint2 c = *reinterpret_cast<const uint2 *>(src);
-      const float scale = *scale_at(kv, tile[r.row], tok[r.row], r);
-      float x[8];
-      decode4<TYPE>(c.x, x);
-      decode4<TYPE>(c.y, x + 4);
-      u.x = pack_bf16x2(x[0] * scale, x[1] * scale);
-      u.y = pack_bf16x2(x[2] * scale, x[3] * scale);
-      u.z = pack_bf16x2(x[4] * scale, x[5] * scale);
-      u.w = pack_bf16x2(x[6] * scale, x[7] * scale);
+  while (from.x < 2 * rows) {
+    uint4 u[kAhead];
+    float scale[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int row = from.x >> 1, which = from.x & 1, head = from.head;
+      const long long at = row < rows ? tile[row] : -1;
+      from.next(kv.heads);
+      u[i] = make_uint4(0, 0, 0, 0);
+      scale[i] = 0.f;
+      if (at < 0) continue;
+      u[i] = *held(kv.base + at, tok[row], which, head);
+      if (TYPE != LORA_KV_BF16) scale[i] = *held.scale(kv.base + at, tok[row], which, head);
     }
-    uint8_t *dst = r.which ? a.v + (first + r.row) * a.ldv : a.k + (first + r.row) * a.ldk;
-    *reinterpret_cast<uint4 *>(dst + (r.head * kv.dim + e) * 2) = u;
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int row = to.x >> 1, which = to.x & 1, head = to.head;
+      to.next(kv.heads);
+      if (row >= rows || tile[row] < 0) continue;
+      uint4 *dst = reinterpret_cast<uint4 *>((which ? dst_v + row * a.ldv : dst_k + row * a.ldk) + head * kv.dim * 2);
+      if (TYPE == LORA_KV_BF16) {
+        __stcs(dst, u[i]);
+        continue;
+      }
+      const uint32_t c[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+#pragma unroll
+      for (int k = 0; k < U; ++k) {
+        float x[8];
+        decode4<TYPE>(c[2 * k], x);
+        decode4<TYPE>(c[2 * k + 1], x + 4);
+        const float m = scale[i];
+        __stcs(dst + k, make_uint4(pack_bf16x2(x[0] * m, x[1] * m), pack_bf16x2(x[2] * m, x[3] * m),
+                                   pack_bf16x2(x[4] * m, x[5] * m), pack_bf16x2(x[6] * m, x[7] * m)));
+      }
+    }
   }
 }
 
@@ -230,11 +314,11 @@ int check_row_call(const lora_kv *kv, int layer, const void *k, int ldk, const v
 
 template <class K>
 int launch_rows(K kernel, const lora_kv *kv, int layer, const KvSeqs &s, RowArgs a, cudaStream_t st) {
-  a.lanes = 2;
-  while (a.lanes * 8 < kv->dim) a.lanes *= 2;
-  const int per_row = 2 * kv->heads * a.lanes;
-  a.rows = 4 * kRowThreads / per_row;
-  a.rows = a.rows < 1 ? 1 : a.rows > kMaxBlockRows ? kMaxBlockRows : a.rows;
+  a.lanes = 1;
+  while (a.lanes * vec_elements(kv->type) < kv->dim) a.lanes *= 2;
+  const int at_once = kv->n_sm * kRowBlocks;
+  a.rows = (a.T + at_once - 1) / at_once;
+  a.rows = a.rows > kMaxBlockRows ? kMaxBlockRows : a.rows;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((a.T + a.rows - 1) / a.rows);
   cfg.blockDim = dim3(kRowThreads);

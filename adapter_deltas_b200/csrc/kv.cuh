@@ -74,33 +74,38 @@ __device__ __forceinline__ long long kv_head_stride(const KvView &kv) {
 // is held as codes and one fp32 scale:
 //     scale = amax / qmax,   code = round_to_nearest_even(x * qmax / amax),
 // qmax = 448 (e4m3) or 127 (int8).  The quotient of two bf16 values often lies
-// exactly half way between two codes, so it is formed correctly rounded: the
-// product with qmax is exact for bf16 x, and the quotient is corrected with
-// its fma residual and the rounded reciprocal of amax (P. Markstein,
-// "Computation of elementary functions on the IBM RISC System/6000 processor",
-// 1990).  From amax 2^64 on both sides are scaled by 2^-64, which keeps the
-// product and the reciprocal in range.  A row whose largest magnitude is below
-// 2^-100 is held as zeros with scale 0 (its scale would lose its bits to
-// underflow); one with an infinity or a NaN has a NaN for its scale, so that
-// all its values read back as NaN.
+// exactly half way between two codes, so such a quotient has to come out exact:
+// the product with qmax is exact for bf16 x, the residual of a first quotient is
+// exact by fma, and the quotient corrected with it rounds to the exact one where
+// that is representable (an approximate reciprocal of amax suffices for both).
+// Every other quotient of bf16 values is further from a tie than fp32's error.
+// The scale's division by a constant is corrected in the same way.  From amax
+// 2^64 on both sides are scaled by 2^-64, which keeps the product and the
+// reciprocal in range.  A row whose largest magnitude is below 2^-100 is held as
+// zeros with scale 0 (its scale would lose its bits to underflow); one with an
+// infinity or a NaN has a NaN for its scale, so that all its values read back as
+// NaN.
 struct Quant {
   float scale;  // what the codes are multiplied by when read
   float mul;    // qmax, times 2^-64 from amax 2^64 on
   float amax;   // in the same scaling
-  float rcp;    // 1 / amax, rounded
+  float rcp;    // about 1 / amax
 };
 
 template <int QMAX>
 __device__ __forceinline__ Quant quant_of(float amax) {
   Quant q;
   const bool none = amax < 0x1p-100f, big = amax >= 0x1p64f;
-  q.scale = none ? 0.f : fmaf(amax, 0.f, __fdiv_rn(amax, (float)QMAX));  // (infinity * 0: NaN)
+  constexpr float kInv = 1.f / QMAX;
+  const float s = amax * kInv;
+  q.scale = none ? 0.f : fmaf(fmaf(-s, (float)QMAX, amax), kInv, s);  // (an infinity: inf - inf)
   q.amax = big ? amax * 0x1p-64f : amax;
   q.mul = none ? 0.f : big ? QMAX * 0x1p-64f : (float)QMAX;
-  q.rcp = none ? 0.f : __frcp_rn(q.amax);
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(q.rcp) : "f"(q.amax));
+  if (none) q.rcp = 0.f;
   return q;
 }
-// x * qmax / amax, correctly rounded.
+// x * qmax / amax.
 __device__ __forceinline__ float quant_div(float x, const Quant &q) {
   const float a = x * q.mul, t = a * q.rcp;
   return fmaf(fmaf(-t, q.amax, a), q.rcp, t);
