@@ -227,7 +227,7 @@ __global__ void __launch_bounds__(kRowThreads, kRowBlocks) kv_append_kernel(KvVi
 
 template <int TYPE>
 __global__ void __launch_bounds__(kRowThreads, kRowBlocks) kv_gather_kernel(KvView kv, KvSeqs s, RowArgs a) {
-  constexpr int E = vec_elements(TYPE), U = E / 8, kAhead = 4 / U;
+  constexpr int E = vec_elements(TYPE), U = E / 8, kAhead = 4;
   __shared__ long long tile[kMaxBlockRows];
   __shared__ int tok[kMaxBlockRows];
   const int first = blockIdx.x * a.rows, rows = min(a.rows, a.T - first);
