@@ -386,17 +386,22 @@ class KvHandle:
         return self.ptr
 
 
+# The calls below run once or twice per layer of a step, some of them for a few
+# microseconds on the GPU: their checks read each property of a tensor once.
+
+
 def _rows(t, name: str, device: int, width: int, dtype, where: str):
-    """A [T, ld] operand of a call that reads or writes T rows of `width` values through its row stride."""
-    if t.dtype != dtype or t.get_device() != device or t.dim() != 2 or t.shape[1] != width or \
-            (width > 1 and t.stride(1) != 1):
+    """Address and leading dimension of a [T, ld] operand whose rows of `width` values are reached by its row stride."""
+    shape, stride = t.shape, t.stride()
+    if t.dtype is not dtype or t.get_device() != device or len(shape) != 2 or shape[1] != width or \
+            (stride[1] != 1 and width > 1):
         raise ValueError("%s: %s must be %s [T, %d] with unit column stride on cuda:%d, not %s %s %s"
-                         % (where, name, dtype, width, device, t.dtype, tuple(t.shape), t.device))
-    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else max(t.stride(0), (width + 7) // 8 * 8)
+                         % (where, name, dtype, width, device, t.dtype, tuple(shape), t.device))
+    return t.data_ptr(), stride[0] if shape[0] > 1 else max(stride[0], (width + 7) // 8 * 8)
 
 
 def _dense(t, name: str, device: int, shape, dtype, where: str) -> int:
-    if t.dtype != dtype or t.get_device() != device or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+    if t.dtype is not dtype or t.get_device() != device or t.shape != shape or not t.is_contiguous():
         raise ValueError("%s: %s must be contiguous %s %s on cuda:%d, not %s %s %s"
                          % (where, name, dtype, tuple(shape), device, t.dtype, tuple(t.shape), t.device))
     return t.data_ptr()
@@ -406,7 +411,7 @@ def _stream_on(stream, device: int) -> int:
     """The stream argument of a call on `device`; the current stream of that device by default."""
     if stream is None:
         import torch
-        return torch.cuda.current_stream(device).cuda_stream
+        return torch._C._cuda_getCurrentRawStream(device)  # (current_stream() makes an object, about 1 us)
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
