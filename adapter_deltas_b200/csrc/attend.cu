@@ -25,8 +25,10 @@
 //    table; there is no block-wide synchronisation until the end.
 //  - A (sequence, unit) that lies inside one warp's range is written at once.
 //    States of ranges that cut one are joined in the block, in token order;
-//    what a block's border cuts goes to the workspace and is joined by a second,
-//    small launch (again in order: equal inputs give equal bits).
+//    what a block's border cuts goes to the workspace, and the last of a unit's
+//    blocks to get there joins them (in order again, whichever block it is:
+//    equal inputs give equal bits).  Blocks count themselves in, none waits for
+//    another.  (As a second launch the join took 4 to 6 us.)
 //
 // The products run on the warp-level tensor instruction (m16n8k16): a unit's 8
 // query heads are the N = 8 of both products, S^T = K q^T (16 tokens x 8 heads)
@@ -49,7 +51,6 @@ namespace lora {
 constexpr int kAttMaxWarps = 12;
 constexpr int kAttMaxStages = 8;
 constexpr int kAttSmem = 227 * 1024;
-constexpr int kJoinThreads = 512;
 constexpr int kSlack = 4, kVSlack = 2;  // powers of two
 
 struct AttendArgs {
@@ -66,11 +67,14 @@ struct AttendArgs {
   int window;
   int n_stages;
   // workspace: what each block's borders cut
-  int4 *cut;           // [blocks] {sequence (-1: none), unit, last block, 0}: a unit that starts in the block and goes on
+  unsigned long long *done;  // [blocks] how many blocks of the unit that starts in a block and goes on are done
+  unsigned long long tag;    // of this launch, in done's upper bits: whatever is there from before counts as none
   float *part;         // [blocks][2] states: 0 continues from the block before, 1 starts here
   float *first;        // [blocks][warps] states: a warp's first piece, when more of its range follows,
   int first_in_smem;   // or where in shared memory those are (0: not there)
 };
+
+constexpr int kCountBits = 16;  // of done
 
 // A state in memory: m[rows], l[rows] (each row's place a multiple of 16 bytes
 // from the start: rows * 2 rounded up to 4 floats), then rows x dim weighted sums.
@@ -195,17 +199,17 @@ __device__ __forceinline__ int unit_slots(int len, int window, int tt) {
 struct Ends {
   float mul, lse;
 };
-__device__ __forceinline__ Ends finish(const AttendArgs &a, int head, float m, float l) {
+__device__ __forceinline__ Ends finish(const float *sinks, int head, float m, float l) {
   Ends e;
   float base = m;
-  if (a.sinks) {
-    const float sink = a.sinks[head] * 1.44269504f;
+  if (sinks) {
+    const float sink = sinks[head] * 1.44269504f;
     base = fmaxf(m, sink);
     l = l * exp2_fast(m - base) + exp2_fast(sink - base);
   }
   e.mul = __fdividef(exp2_fast(m - base), l);
-  if (m == -INFINITY && !a.sinks) e.mul = __int_as_float(0x7fc00000);  // (every score minus infinity: 0 / 0)
-  e.lse = fmaf(base, 0.693147181f, logf(l));
+  if (m == -INFINITY && !sinks) e.mul = __int_as_float(0x7fc00000);  // (every score minus infinity: 0 / 0)
+  e.lse = fmaf(base, 0.693147181f, 0.693147181f * __log2f(l));
   return e;
 }
 
@@ -215,6 +219,15 @@ __device__ __forceinline__ Ends finish(const AttendArgs &a, int head, float m, f
 struct Step {
   int seq, unit, pos, len;  // sequence, unit, first token of the step, tokens of the sequence
 };
+// A unit as its key head and the first of its query heads in that head's group, in one number.
+__device__ __forceinline__ int pack_unit(int kvh, int h0) { return kvh << 16 | h0; }
+__device__ __forceinline__ int unit_kvh(int unit) { return unit >> 16; }
+__device__ __forceinline__ int unit_h0(int unit) { return unit & 0xffff; }
+
+// a / b, without the long division where 32 bits do (a call: it is used in places that run once).
+__device__ __noinline__ unsigned long long quotient(unsigned long long a, unsigned long long b) {
+  return (a | b) >> 32 ? a / b : (unsigned)a / (unsigned)b;
+}
 
 // DIM: the head's width, or with ANY the largest of a range of multiples of 16 (kv.dim is the width).
 // TT: tiles of 16 tokens per step.  WARPS: most warps of a block.  NT: 8 NT query heads to a unit.
@@ -231,12 +244,14 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(KvView kv, KvSeqs
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint64_t full[kAttMaxWarps][kAttMaxStages];
   __shared__ Step held[kAttMaxWarps][kAttMaxStages];
-  __shared__ long long scan[kAttMaxWarps], from[kAttMaxWarps];  // from: a warp's first slot, from its sequence's first
-  __shared__ int2 start[kAttMaxWarps];                          // {sequence, length} of it
+  // a warp's first slot, from its sequence's first, and that sequence and its length; last entry: the block's last slot
+  __shared__ long long scan[kAttMaxWarps], from[kAttMaxWarps + 1];
+  __shared__ int2 start[kAttMaxWarps + 1];
   __shared__ int4 piece[2 * kAttMaxWarps];  // [2 warp + which]: {sequence (-1: none), unit, cut before 1 / after 2, -}
   __shared__ const float *where[2 * kAttMaxWarps];
   __shared__ int order[2 * kAttMaxWarps], run[2 * kAttMaxWarps + 1];  // pieces in order; where each unit's run starts
-  __shared__ int n_runs, dead_block, tail_steps;  // tail_steps: of the unit that the block's end cuts, behind it
+  __shared__ int n_runs, dead_block;
+  __shared__ int2 to_join[2];  // {first block, blocks} of units that this block was the last to work on
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int n_warps = blockDim.x >> 5;
@@ -253,6 +268,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(KvView kv, KvSeqs
   const int per = (s.n + blockDim.x - 1) / blockDim.x;
   const int s0 = min(s.n, tid * per), s1 = min(s.n, s0 + per);
   long long mine = 0;
+#pragma unroll 1
   for (int i = s0; i < s1; ++i) mine += unit_slots(seq_len(kv, s, i), a.window, TT);
   long long before = mine;  // inclusive scan over the block
 #pragma unroll
@@ -274,23 +290,20 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(KvView kv, KvSeqs
   // every block in a row having a part)
   const unsigned long long slots_all = (unsigned long long)total * a.units;
   const unsigned blocks = (unsigned)min((unsigned long long)gridDim.x, slots_all / 2);
-  unsigned long long each = 0;  // slots of a block; the first `more` have one more
-  unsigned more = 0;
-  if (slots_all >> 32)
-    each = slots_all / max(blocks, 1u);
-  else
-    each = (unsigned)slots_all / max(blocks, 1u);
-  more = (unsigned)(slots_all - each * blocks);
+  const unsigned long long each = quotient(slots_all, max(blocks, 1u));  // slots of a block; the first `more` have one more
+  const unsigned more = (unsigned)(slots_all - each * blocks);
   const long long b0 = each * blockIdx.x + min(blockIdx.x, more);
   const int slots = blockIdx.x < blocks ? (int)each + (blockIdx.x < more) : 0;
   const int wq = slots / n_warps, wr = slots - wq * n_warps;
   if (mine > 0) {  // whose range starts in this thread's sequences
     const long long lo = before * a.units - b0, hi = lo + mine * a.units;
     if (lo < slots && hi > 0) {
-      for (int w = 0; w < n_warps; ++w) {
-        const int at = wq * w + min(w, wr);
+#pragma unroll 1
+      for (int w = 0; w <= n_warps; ++w) {
+        const int at = w < n_warps ? wq * w + min(w, wr) : slots - 1;
         if (at < lo || at >= hi || at >= slots) continue;
         long long p = lo;
+#pragma unroll 1
         for (int i = s0; i < s1; ++i) {
           const int len = seq_len(kv, s, i);
           const long long e = p + (long long)unit_slots(len, a.window, TT) * a.units;
@@ -313,27 +326,21 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(KvView kv, KvSeqs
     int left = count;  // slots not yet passed
     int fetched = 0;   // steps fetched or being so
     int fseq = start[warp].x, flen = start[warp].y;
-    int funit, fpos;   // fpos: first token of the step
-    bool fnew = true;  // the step to fetch is the first of a unit or of the range
-    bool own_slot;     // the unit's own slot is to be passed first
+    int fkvh, fh0, fpos;  // the unit's key head and first query head; first token of the step
+    bool fnew = true;     // the step to fetch is the first of a unit or of the range
+    bool own_slot;        // the unit's own slot is to be passed first
     {
-      const int n = unit_slots(flen, a.window, TT);
-      const unsigned long long off = from[warp];
-      int step;
-      if (off >> 32) {
-        funit = (int)(off / (unsigned)n);
-        step = (int)(off - (unsigned long long)funit * n);
-      } else {
-        funit = (int)((unsigned)off / (unsigned)n);
-        step = (int)((unsigned)off - (unsigned)funit * n);
-      }
-      own_slot = step == 0;
-      fpos = (first_token(flen, a.window) / kStep + max(step - 1, 0)) * kStep;
+      const int n = unit_slots(flen, a.window, TT), unit = (int)quotient(from[warp], n);
+      const int slot = (int)(from[warp] - (long long)unit * n);
+      own_slot = slot == 0;
+      fpos = (first_token(flen, a.window) / kStep + max(slot - 1, 0)) * kStep;
+      fkvh = a.head_groups == 1 ? unit : unit / a.head_groups;
+      fh0 = (unit - fkvh * a.head_groups) * ROWS;
     }
     const bool starts_inside = fpos > first_token(flen, a.window);  // of its unit
     unsigned bad_tiles = 0;     // bits stage * TT ..: tiles of a stage that are on no page of the cache
     const long long head_stride = kv_head_stride(kv);
-    const uint8_t *fhead = kv.base + (funit / a.head_groups) * head_stride;
+    const uint8_t *fhead = kv.base + fkvh * head_stride;
     // a step's tiles lie in one page, one behind the other, unless pages are shorter
     const bool one_copy = TT == 1 || (1 << kv.log2_page) >= kStep;
     // lane i: page of the sequence's tile base + i, or -1
@@ -345,7 +352,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(KvView kv, KvSeqs
     // the sequence after: its length is read when this one begins, its first pages when this one's last unit does
     int nlen = fseq + 1 < s.n ? __ldg(s.lens + fseq + 1) : 0, npages = 0;
     auto load_next = [&]() {
-      if (funit != a.units - 1 || fseq + 1 >= s.n) return;
+      if (fkvh != kv.heads - 1 || fh0 + ROWS < a.group || fseq + 1 >= s.n) return;
       nlen = valid_len(kv, s, nlen);
       npages = load_pages(fseq + 1, nlen, first_token(nlen, a.window) / kStep * TT & ~31);
     };
@@ -374,7 +381,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(KvView kv, KvSeqs
       int n = at >= 0 ? t1 - t0 : 0;
       if (TT > 1 && !one_copy) n = __popc(__ballot_sync(~0u, copy));
       if (lane == 0) {
-        if (fnew) held[warp][stage] = {fseq, funit, fpos, flen};
+        if (fnew) held[warp][stage] = {fseq, pack_unit(fkvh, fh0), fpos, flen};
         mbar_arrive_expect_tx(&full[warp][stage], n * tile_bytes);
       }
       if (n < t1 - t0) {
@@ -390,13 +397,21 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(KvView kv, KvSeqs
       fnew = fpos >= flen;
       if (fnew) {
         own_slot = true;
-        if (++funit == a.units) {
-          funit = 0;
+        fh0 += ROWS;
+        if (fh0 >= a.group) {
+          fh0 = 0;
+          ++fkvh;
+          fhead += head_stride;
+        }
+        if (fkvh == kv.heads) {
+          fkvh = 0;
+          fhead = kv.base;
           if (left > 1) {  // (another step is to come)
             ++fseq;
             flen = valid_len(kv, s, nlen);
             pages = npages;
             pbase = first_token(flen, a.window) / kStep * TT & ~31;
+#pragma unroll 1
             while (flen == 0) {
               ++fseq;
               flen = seq_len(kv, s, fseq);
@@ -406,7 +421,6 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(KvView kv, KvSeqs
           }
         }
         fpos = first_token(flen, a.window) / kStep * kStep;
-        fhead = kv.base + (funit / a.head_groups) * head_stride;
         load_next();
       }
     };
@@ -435,7 +449,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(KvView kv, KvSeqs
 
     // q as the products' B operand: columns = heads, rows = dims in the order of the K operand
     auto load_q = [&]() {
-      const int kvh = cunit / a.head_groups, h0 = (cunit - kvh * a.head_groups) * ROWS, j = lane & 3;
+      const int kvh = unit_kvh(cunit), h0 = unit_h0(cunit), j = lane & 3;
 #pragma unroll
       for (int h = 0; h < NT; ++h) {
         const bool live = h0 + g + 8 * h < a.group;
@@ -479,11 +493,15 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(KvView kv, KvSeqs
           float x[4] = {bf16_lo(u[b].x) * mul, bf16_hi(u[b].x) * mul, bf16_lo(u[b].y) * mul, bf16_hi(u[b].y) * mul};
           if (FORM == kInt8) {
 #pragma unroll
-            for (int k = 0; k < 3; ++k) {
-              const uint32_t t = int8x4(x[0], x[1], x[2], x[3]);
-              qa[h][(b >> 1) * 6 + 2 * k + (b & 1)] = t;
+            for (int k = 0; k < 3; ++k) {  // adding 1.5 * 2^23 rounds to an integer, in the sum's low bits
+              float y[4];
 #pragma unroll
-              for (int e = 0; e < 4; ++e) x[e] = (x[e] - (float)(int8_t)(t >> (8 * e))) * 128.f;
+              for (int e = 0; e < 4; ++e) y[e] = x[e] + 12582912.f;
+              const uint32_t lo = __byte_perm(__float_as_uint(y[0]), __float_as_uint(y[1]), 0x0040);
+              const uint32_t hi = __byte_perm(__float_as_uint(y[2]), __float_as_uint(y[3]), 0x0040);
+              qa[h][(b >> 1) * 6 + 2 * k + (b & 1)] = __byte_perm(lo, hi, 0x5410);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) x[e] = (x[e] - (y[e] - 12582912.f)) * 128.f;
             }
           } else {  // as key_codes_to_f16 pairs the dims
             qa[h][b * 2] = TYPE == LORA_KV_E4M3 ? pack_f16x2(x[0], x[1]) : pack_f16x2(x[0], x[2]);
@@ -494,27 +512,29 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(KvView kv, KvSeqs
     };
 
     // (the first iterations fill the ring: one place in the code for each part)
+#pragma unroll 1
     for (int i = 1 - a.n_stages;; ++i) {
+      asm volatile("" : "+r"(i));  // (one copy of the loop's body, not one for the filling)
       fetch(fstage);
       if (++fstage == a.n_stages) fstage = 0;
       if (i < 0) continue;
-      const bool end = i == fetched;
-      if (end || cnew) {
+      int leaving = i == fetched ? 2 : cnew;  // (opaque, for the same reason)
+      asm volatile("" : "+r"(leaving));
+      if (leaving) {
         if (cseq >= 0) {
           // The unit's state leaves the registers: as its result when the warp
           // has seen all of it, else as a piece to be joined (at the range's end
           // the ring is free for it).
-          const bool cut_after = end && !cnew;
+          const bool cut_after = leaving == 2 && !cnew;
           const bool whole = !cut_before && !cut_after;
-          const int kvh = cunit / a.head_groups, h0 = (cunit - kvh * a.head_groups) * ROWS;
-          float *state = end ? reinterpret_cast<float *>(ring) : a.first_in_smem
+          const int kvh = unit_kvh(cunit), h0 = unit_h0(cunit);
+          float *state = leaving == 2 ? reinterpret_cast<float *>(ring) : a.first_in_smem
                              ? reinterpret_cast<float *>(smem + a.first_in_smem) + warp * floats
                              : a.first + ((size_t)blockIdx.x * kAttMaxWarps + warp) * floats;
           if (!whole && lane == 0) {
             const int k = 2 * warp + (cut_before ? 0 : 1);
             piece[k] = make_int4(cseq, cunit, (cut_before ? 1 : 0) | (cut_after ? 2 : 0), 0);
             where[k] = state;
-            if (cut_after && warp == (wq ? n_warps : wr) - 1) tail_steps = (clen - cpos + kStep - 1) / kStep;  // (the block's last steps)
           }
 #pragma unroll
           for (int h = 0; h < NT; ++h) {
@@ -530,7 +550,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(KvView kv, KvSeqs
               mul[e] = TYPE == LORA_KV_BF16 ? 1.f : vtop / exp2_int(15 - kSlack - kVSlack);
               if (!on[e]) continue;
               if (whole) {
-                const Ends x = finish(a, hd, m[h][e], l[h][e]);
+                const Ends x = finish(a.sinks, hd, m[h][e], l[h][e]);
                 mul[e] *= x.mul;
                 if (a.lse && g == 0) a.lse[(long long)cseq * a.n_heads + hd] = x.lse;
               } else if (g == 0) {
@@ -541,35 +561,40 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(KvView kv, KvSeqs
             const int r = 8 * h + j2;
             float *sums = state + state_head(a.rows) + r * dim;
             uint8_t *out = a.out + cseq * a.ldo + (long long)(kvh * a.group + h0 + r) * dim * 2;
+            // a thread's two neighbouring dims of each of its two heads; 8 bits:
+            // rows g and g + 8 are dims 2 g and 2 g + 1; bf16: dims g and g + 8, and
+            // neighbouring rows trade one
+            const int d0 = TYPE != LORA_KV_BF16 ? 2 * g : g & 1 ? 7 + g : g;
+            auto pair_of = [&](int b, int e) {
+              float2 x = make_float2(o[h][b][e], o[h][b][2 + e]);
+              if (TYPE == LORA_KV_BF16) {
+                const float got = __shfl_xor_sync(~0u, g & 1 ? x.x : x.y, 4);
+                x = g & 1 ? make_float2(got, x.y) : make_float2(x.x, got);
+              }
+              return make_float2(x.x * mul[e], x.y * mul[e]);
+            };
+            if (whole) {
 #pragma unroll
-            for (int b = 0; b < NB; ++b) {
-              if (ANY && b >= nb) continue;
-              // a thread's two neighbouring dims of each of its two heads
-              int d = 16 * b + 2 * g;  // 8 bits: rows g and g + 8 are dims 2 g and 2 g + 1
-              float x[2][2];
+              for (int b = 0; b < NB; ++b)
 #pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                x[e][0] = o[h][b][e];
-                x[e][1] = o[h][b][2 + e];
-                if (TYPE == LORA_KV_BF16) {  // dims g and g + 8: neighbouring rows trade
-                  const float got = __shfl_xor_sync(~0u, g & 1 ? x[e][0] : x[e][1], 4);
-                  x[e][0] = g & 1 ? got : x[e][0];
-                  x[e][1] = g & 1 ? x[e][1] : got;
+                for (int e = 0; e < 2; ++e) {
+                  if (ANY && b >= nb) continue;
+                  const float2 x = pair_of(b, e);
+                  if (on[e]) *reinterpret_cast<uint32_t *>(out + (e * dim + 16 * b + d0) * 2) = pack_bf16x2(x.x, x.y);
                 }
-              }
-              if (TYPE == LORA_KV_BF16) d = 16 * b + (g & 1 ? 7 + g : g);
+            } else {
 #pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                if (!on[e]) continue;
-                if (whole)
-                  *reinterpret_cast<uint32_t *>(out + (e * dim + d) * 2) = pack_bf16x2(x[e][0] * mul[e], x[e][1] * mul[e]);
-                else
-                  *reinterpret_cast<float2 *>(sums + e * dim + d) = make_float2(x[e][0] * mul[e], x[e][1] * mul[e]);
-              }
+              for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  if (ANY && b >= nb) continue;
+                  const float2 x = pair_of(b, e);
+                  if (on[e]) *reinterpret_cast<float2 *>(sums + e * dim + 16 * b + d0) = x;
+                }
             }
           }
         }
-        if (end) break;
+        if (leaving == 2) break;
         cut_before = i == 0 && starts_inside;
         const Step st = held[warp][stage];
         cseq = st.seq;
@@ -586,16 +611,20 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(KvView kv, KvSeqs
         }
         vtop = unit = 0.f;
         load_q();
-        {  // the next unit's q, towards this SM
-          const bool same = cunit + 1 < a.units;
-          const int nu = same ? cunit + 1 : 0, ns = cseq + !same, bytes = a.rows * dim * 2;
-          const uint8_t *q = a.q + ns * a.ldq + ((nu / a.head_groups) * a.group + (nu % a.head_groups) * ROWS) * (long long)dim * 2;
-          if (ns < s.n)
+        {  // the next unit's q, towards this SM: the rows behind, or the next sequence's first
+          const int kvh = unit_kvh(cunit), h0 = unit_h0(cunit);
+          const bool last = kvh == kv.heads - 1 && h0 + ROWS >= a.group;
+          const uint8_t *q = last ? a.q + (cseq + 1) * a.ldq
+                                  : a.q + cseq * a.ldq + (long long)(kvh * a.group + min(h0 + ROWS, a.group)) * dim * 2;
+          const int bytes = a.rows * dim * 2;
+          if (!last || cseq + 1 < s.n)
+#pragma unroll 1
             for (int x = lane * 128; x < bytes; x += 32 * 128) asm volatile("prefetch.global.L1 [%0];" ::"l"(q + x));
         }
       }
       if (!mbar_wait_bounded(&full[warp][stage], phase, kv.status)) {
         // copies in flight must land before the block ends (again a bounded wait)
+#pragma unroll 1
         for (int k = 0; k < a.n_stages; ++k) (void)mbar_wait_bounded(&full[warp][k], phase ^ (k < stage), kv.status);
         if (lane == 0) dead_block = 1;
         break;
@@ -611,6 +640,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(KvView kv, KvSeqs
       cnew = cpos >= clen;
       if (TYPE != LORA_KV_INT8 && partial) {
         // weight 0 times what lies there must be 0: clear V's rows outside (int8 has no NaN)
+#pragma unroll 1
         for (int x = lane; x < kStep * chunks; x += 32) {
           const int t = x / chunks;
           if (t >= lo && t < hi && !(bad >> (t / kTileTokens) & 1)) continue;
@@ -852,33 +882,20 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(KvView kv, KvSeqs
       n_runs = __popc(firsts);
       run[__popc(firsts)] = __popc(there);
     }
-    // the last run goes on past the block and starts in it: the join finishes it, up to its last step's block
-    int4 cut = make_int4(-1, 0, 0, 0);
-    const int last_first = firsts ? 31 - __clz(firsts) : 0, last = there ? 31 - __clz(there) : 0;
-    const int head_cut = __shfl_sync(~0u, p.z, last_first), tail_cut = __shfl_sync(~0u, p.z, last);
-    cut.x = __shfl_sync(~0u, p.x, last);
-    cut.y = __shfl_sync(~0u, p.y, last);
-    if (!there || broken || !(tail_cut & 2) || (head_cut & 1)) {
-      cut.x = -1;
-    } else {
-      const unsigned long long slot = b0 + slots + tail_steps - 1, big = (each + 1) * more;
-      cut.z = (int)(slot < big ? slot / (each + 1) : more + (slot - big) / each);
-    }
-    if (lane == 0) a.cut[blockIdx.x] = cut;
   }
-  if (broken && tid < 2 * a.rows)  // (no result for what this block was to add to)
-    a.part[((size_t)blockIdx.x * 2 + tid / a.rows) * floats + a.rows + tid % a.rows] = -1.f;
   __syncthreads();
   const int quads = dim / 4;
   const int per_run = a.rows * quads;
+#pragma unroll 1
   for (int i0 = tid; i0 < n_runs * per_run && !broken; i0 += blockDim.x) {
     const int k = i0 / per_run, r = (i0 - k * per_run) / quads, d = (i0 - k * per_run - r * quads) * 4;
     const int f = run[k], e = run[k + 1];
     const int4 p0 = piece[order[f]], p1 = piece[order[e - 1]];
     const bool whole = !(p0.z & 1) && !(p1.z & 2);
-    const int kvh = p0.y / a.head_groups, h0 = (p0.y - kvh * a.head_groups) * ROWS;
+    const int kvh = unit_kvh(p0.y), h0 = unit_h0(p0.y);
     if (h0 + r >= a.group) continue;
     float mm = -INFINITY, ll = 0.f;
+#pragma unroll 1
     for (int i = f; i < e; ++i) mm = fmaxf(mm, where[order[i]][r]);
     const float bm = mm == -INFINITY ? 0.f : mm;
     float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -895,7 +912,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(KvView kv, KvSeqs
     }
     if (whole) {
       const int hd = kvh * a.group + h0 + r;
-      const Ends fin = finish(a, hd, mm, ll);
+      const Ends fin = finish(a.sinks, hd, mm, ll);
       if (a.lse && d == 0) a.lse[(long long)p0.x * a.n_heads + hd] = fin.lse;
       *reinterpret_cast<uint2 *>(a.out + p0.x * a.ldo + ((long long)hd * dim + d) * 2) =
           make_uint2(pack_bf16x2(y.x * fin.mul, y.y * fin.mul), pack_bf16x2(y.z * fin.mul, y.w * fin.mul));
@@ -909,7 +926,115 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(KvView kv, KvSeqs
     }
   }
 
+  __syncthreads();
+
+  // ---- count this block in for the units its borders cut (thread 0: the one it
+  // begins in, thread 32: the one it ends in); the last of a unit's blocks joins
+  if (tid == 0 || tid == 32) {
+    const int which = tid >> 5;
+    to_join[which] = make_int2(0, 0);
+    if (slots > 0) {
+      const int at = which ? n_warps : 0;
+      const int n = unit_slots(start[at].y, a.window, TT);
+      const int in = (int)(from[at] - quotient(from[at], n) * n);  // slot of its unit
+      // the unit's first and last step's slots in the list
+      const long long here = which ? b0 + slots - 1 : b0, s_first = here - in + 1, s_last = here - in + n - 1;
+      const bool cut = which ? in > 0 && s_last > here && s_first >= b0 : in > 1;
+      if (cut) {
+        auto block_of = [&](unsigned long long slot) {
+          const unsigned long long big = (each + 1) * more;
+          return (int)(slot < big ? quotient(slot, each + 1) : more + quotient(slot - big, each));
+        };
+        const int b_first = block_of(s_first), b_last = block_of(s_last);
+        if (broken)  // (no result for what this block was to add to)
+#pragma unroll 1
+          for (int r = 0; r < a.rows; ++r) a.part[((size_t)blockIdx.x * 2 + which) * floats + a.rows + r] = -1.f;
+        __threadfence();
+        unsigned long long seen = atomicAdd(a.done + b_first, 0ull), next;
+        do {
+          next = (seen >> kCountBits) == a.tag ? seen + 1 : a.tag << kCountBits | 1;
+          const unsigned long long was = atomicCAS(a.done + b_first, seen, next);
+          if (was == seen) break;
+          seen = was;
+        } while (true);
+        __threadfence();
+        if ((int)(next & ((1u << kCountBits) - 1u)) == b_last - b_first + 1) {
+          a.done[b_first] = 0;
+          to_join[which] = make_int2(b_first, b_last - b_first + 1);
+        }
+      }
+    }
+  }
+  __syncthreads();
+#pragma unroll 1
+  for (int which = 0; which < 2; ++which) {
+    const int2 job = to_join[which];
+    if (!job.y) continue;
+    const int unit = which ? n_warps : 0, seq = start[unit].x;
+    const int un = (int)quotient(from[unit], unit_slots(start[unit].y, a.window, TT));
+    const int kvh = un / a.head_groups, h0 = (un - kvh * a.head_groups) * ROWS, live = min(a.rows, a.group - h0);
+    // the first block's own part (1), then those after it (0)
+    auto state = [&](int i) { return a.part + ((size_t)(job.x + i) * 2 + (i ? 0 : 1)) * floats; };
+    float *weight = reinterpret_cast<float *>(smem);  // [parts][rows], behind it [rows] maxima and sums (the rings are idle)
+    float *tops = weight + job.y * a.rows, *totals = tops + a.rows;
+#pragma unroll 1
+    for (int r = warp; r < live; r += n_warps) {
+      float mm = -INFINITY, ll = 0.f;
+      bool none = false;
+#pragma unroll 1
+      for (int i = lane; i < job.y; i += 32) {
+        mm = fmaxf(mm, __ldcg(state(i) + r));
+        none |= __ldcg(state(i) + a.rows + r) < 0.f;
+      }
+      for (int d = 16; d; d >>= 1) mm = fmaxf(mm, __shfl_xor_sync(~0u, mm, d));
+      const float bm = mm == -INFINITY ? 0.f : mm;
+#pragma unroll 1
+      for (int i = lane; i < job.y; i += 32) {
+        const float w = exp2_fast(__ldcg(state(i) + r) - bm);
+        weight[i * a.rows + r] = w;
+        ll = fmaf(w, __ldcg(state(i) + a.rows + r), ll);
+      }
+      for (int d = 16; d; d >>= 1) ll += __shfl_xor_sync(~0u, ll, d);
+      if (__any_sync(~0u, none)) ll = -1.f;
+      if (lane == 0) {
+        tops[r] = mm;
+        totals[r] = ll;
+      }
+    }
+    __syncthreads();
+#pragma unroll 1
+    for (int x = tid; x < live * quads; x += blockDim.x) {
+      const int r = x / quads, d = (x - r * quads) * 4;
+      const float ll = totals[r];
+      if (ll < 0.f) continue;  // (a block that gave up: the row stays as it was)
+      const float *at = state(0) + state_head(a.rows) + r * dim + d;
+      float4 y = __ldcg(reinterpret_cast<const float4 *>(at));
+      const float w0 = weight[r];
+      y.x *= w0;
+      y.y *= w0;
+      y.z *= w0;
+      y.w *= w0;
+      at = state(1) + state_head(a.rows) + r * dim + d;
+#pragma unroll 4
+      for (int i = 1; i < job.y; ++i) {
+        const float4 z = __ldcg(reinterpret_cast<const float4 *>(at + (size_t)(i - 1) * 2 * floats));
+        const float w = weight[i * a.rows + r];
+        y.x = fmaf(w, z.x, y.x);
+        y.y = fmaf(w, z.y, y.y);
+        y.z = fmaf(w, z.z, y.z);
+        y.w = fmaf(w, z.w, y.w);
+      }
+      const int hd = kvh * a.group + h0 + r;
+      const Ends e = finish(a.sinks, hd, tops[r], ll);
+      if (a.lse && d == 0) a.lse[(long long)seq * a.n_heads + hd] = e.lse;
+      *reinterpret_cast<uint2 *>(a.out + seq * a.ldo + ((long long)hd * dim + d) * 2) =
+          make_uint2(pack_bf16x2(y.x * e.mul, y.y * e.mul), pack_bf16x2(y.z * e.mul, y.w * e.mul));
+    }
+    __syncthreads();
+  }
+
   // ---- sequences without a token: zeros, or untouched (length -1, and lengths in error)
+#pragma unroll 1
   for (int i0 = blockIdx.x + warp * 32 * gridDim.x; i0 < s.n; i0 += gridDim.x * blockDim.x) {
     const int i = i0 + lane * gridDim.x;
     int len = 1;
@@ -922,88 +1047,14 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(KvView kv, KvSeqs
       const int z = __ffs(empty) - 1;
       empty &= empty - 1;
       const int q = i0 + z * gridDim.x;
+#pragma unroll 1
       for (int c = lane; c < a.n_heads * dim / 8; c += 32)
         *reinterpret_cast<uint4 *>(a.out + q * a.ldo + c * 16) = make_uint4(0, 0, 0, 0);
       if (a.lse)
+#pragma unroll 1
         for (int h = lane; h < a.n_heads; h += 32)
           a.lse[(long long)q * a.n_heads + h] = a.sinks ? a.sinks[h] : -INFINITY;
     }
-  }
-}
-
-// Joins the states of the units that a block's end cut: block b's own (part 1),
-// then those of the blocks after it (part 0) up to the unit's last.  A thread
-// has 4 dims of one head and every SPLITS-th state; the splits meet in shared
-// memory.
-__global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(AttendArgs a, int unit_rows, int dim) {
-  __shared__ float sums[kJoinThreads * 4];
-  __shared__ float tops[16], lens[kJoinThreads];
-  __shared__ int broken;
-  griddep_wait();
-  griddep_launch_dependents();
-  const int4 cut = a.cut[blockIdx.x];
-  if (cut.x < 0) return;
-  const int rows = a.rows, floats = state_floats(rows, dim), n = cut.z - blockIdx.x + 1;
-  auto state = [&](int i) { return a.part + ((size_t)(blockIdx.x + i) * 2 + (i ? 0 : 1)) * floats; };
-  const int h0 = (cut.y % a.head_groups) * unit_rows, live = min(rows, a.group - h0);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  if (tid == 0) broken = 0;
-  __syncthreads();
-  for (int r = warp; r < live; r += kJoinThreads / 32) {
-    float mm = -INFINITY;
-    bool bad = false;
-    for (int i = lane; i < n; i += 32) {
-      mm = fmaxf(mm, state(i)[r]);
-      bad |= state(i)[rows + r] < 0.f;
-    }
-    for (int d = 16; d; d >>= 1) mm = fmaxf(mm, __shfl_xor_sync(~0u, mm, d));
-    if (__any_sync(~0u, bad) && lane == 0) broken = 1;
-    if (lane == 0) tops[r] = mm;
-  }
-  __syncthreads();
-  if (broken) return;
-  const int per = dim / 4;                      // threads of a row
-  const int at_once = max(1, kJoinThreads / per), splits = max(1, at_once / live);
-  for (int r0 = 0; r0 < live; r0 += at_once) {  // (more than one pass only for 16 wide rows)
-    const int slot = tid / per, d = (tid % per) * 4;
-    const int r = r0 + slot / splits, sp = slot % splits;
-    const bool on = slot < at_once && r < live;
-    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-    float ll = 0.f, mm = 0.f;
-    if (on) {
-      mm = tops[r];
-      const float bm = mm == -INFINITY ? 0.f : mm;
-#pragma unroll 4
-      for (int i = sp; i < n; i += splits) {
-        const float *st = state(i);
-        const float w = exp2_fast(st[r] - bm);
-        const float4 y = *reinterpret_cast<const float4 *>(st + state_head(rows) + r * dim + d);
-        ll = fmaf(w, st[rows + r], ll);
-        x.x = fmaf(w, y.x, x.x);
-        x.y = fmaf(w, y.y, x.y);
-        x.z = fmaf(w, y.z, x.z);
-        x.w = fmaf(w, y.w, x.w);
-      }
-      *reinterpret_cast<float4 *>(sums + tid * 4) = x;
-      lens[tid] = ll;
-    }
-    __syncthreads();
-    if (on && sp == 0) {
-      for (int k = 1; k < splits; ++k) {
-        const float4 y = *reinterpret_cast<const float4 *>(sums + (tid + k * per) * 4);
-        x.x += y.x;
-        x.y += y.y;
-        x.z += y.z;
-        x.w += y.w;
-        ll += lens[tid + k * per];
-      }
-      const int hd = (cut.y / a.head_groups) * a.group + h0 + r;
-      const Ends e = finish(a, hd, mm, ll);
-      if (a.lse && d == 0) a.lse[(long long)cut.x * a.n_heads + hd] = e.lse;
-      *reinterpret_cast<uint2 *>(a.out + cut.x * a.ldo + ((long long)hd * dim + d) * 2) =
-          make_uint2(pack_bf16x2(x.x * e.mul, x.y * e.mul), pack_bf16x2(x.z * e.mul, x.w * e.mul));
-    }
-    __syncthreads();
   }
 }
 
@@ -1062,6 +1113,13 @@ Geometry geometry(int most, int stage_bytes, int state_bytes) {
   return g;
 }
 
+// A number for each launch of the process, spread over 48 bits so that what a
+// workspace holds from another use does not look like one.
+unsigned long long next_tag() {
+  static std::atomic<uint64_t> n{1};
+  return n.fetch_add(1) * 0x9e3779b97f4aull % ((1ull << 48) - 1) + 1;
+}
+
 int group_of(const lora_kv *kv, int n_heads) { return n_heads / kv->heads; }
 
 }  // namespace
@@ -1078,7 +1136,7 @@ int attend_setup(lora_kv *kv) {
 size_t attend_workspace_bytes(const lora_kv *kv, int n_heads) {
   const int group = group_of(kv, n_heads);
   const size_t state = size_t(state_floats(group > 16 ? 16 : group, kv->dim)) * 4;
-  return align256(size_t(kv->n_sm) * sizeof(int4)) + size_t(kv->n_sm) * (2 + kAttMaxWarps) * state;
+  return align256(size_t(kv->n_sm) * 8) + size_t(kv->n_sm) * (2 + kAttMaxWarps) * state;
 }
 
 int launch_attend(const lora_kv *kv, int layer, const KvSeqs &s, const AttendCall &c, cudaStream_t st) {
@@ -1104,8 +1162,9 @@ int launch_attend(const lora_kv *kv, int layer, const KvSeqs &s, const AttendCal
   a.n_stages = g.stages;
   a.first_in_smem = g.first;
   uint8_t *ws = static_cast<uint8_t *>(c.ws);
-  a.cut = reinterpret_cast<int4 *>(ws);
-  a.part = reinterpret_cast<float *>(ws + align256(size_t(kv->n_sm) * sizeof(int4)));
+  a.done = reinterpret_cast<unsigned long long *>(ws);
+  a.tag = next_tag();
+  a.part = reinterpret_cast<float *>(ws + align256(size_t(kv->n_sm) * 8));
   a.first = a.part + size_t(kv->n_sm) * 2 * floats;
 
   cudaLaunchConfig_t cfg = {};
@@ -1117,12 +1176,7 @@ int launch_attend(const lora_kv *kv, int layer, const KvSeqs &s, const AttendCal
   attr[0] = pdl_attribute();
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  int rc = cuda_status(cudaLaunchKernelEx(&cfg, v.kernel[wide], kv->view(layer), s, a));
-  if (rc != LORA_OK) return rc;
-  g_launches.fetch_add(1);
-  cfg.blockDim = dim3(kJoinThreads);
-  cfg.dynamicSmemBytes = 0;
-  rc = cuda_status(cudaLaunchKernelEx(&cfg, attend_join_kernel, a, unit_rows, kv->dim));
+  const int rc = cuda_status(cudaLaunchKernelEx(&cfg, v.kernel[wide], kv->view(layer), s, a));
   if (rc == LORA_OK) g_launches.fetch_add(1);
   return rc;
 }
