@@ -52,6 +52,7 @@ constexpr int kAttMaxWarps = 12;
 constexpr int kAttMaxStages = 8;
 constexpr int kAttSmem = 227 * 1024;
 constexpr int kSlack = 4, kVSlack = 2;  // powers of two
+constexpr int kCutSteps = 3;
 
 struct AttendArgs {
   const uint8_t *q;
@@ -245,7 +246,8 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(KvView kv, KvSeqs
   __shared__ uint64_t full[kAttMaxWarps][kAttMaxStages];
   __shared__ Step held[kAttMaxWarps][kAttMaxStages];
   // a warp's first slot, from its sequence's first, and that sequence and its length; last entry: the block's last slot
-  __shared__ long long scan[kAttMaxWarps], from[kAttMaxWarps + 1];
+  __shared__ longlong2 scan[kAttMaxWarps];
+  __shared__ long long from[kAttMaxWarps + 1];
   __shared__ int2 start[kAttMaxWarps + 1];
   __shared__ int4 piece[2 * kAttMaxWarps];  // [2 warp + which]: {sequence (-1: none), unit, cut before 1 / after 2, -}
   __shared__ const float *where[2 * kAttMaxWarps];
@@ -267,33 +269,80 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(KvView kv, KvSeqs
   // ---- this block's and this warp's range of the flat list
   const int per = (s.n + blockDim.x - 1) / blockDim.x;
   const int s0 = min(s.n, tid * per), s1 = min(s.n, s0 + per);
+  // (slots of a unit, summed, and sequences with a token, counted in the bits above)
+  constexpr int kCountAt = 42;
   long long mine = 0;
+  unsigned longest = 0;
 #pragma unroll 1
-  for (int i = s0; i < s1; ++i) mine += unit_slots(seq_len(kv, s, i), a.window, TT);
+  for (int i = s0; i < s1; ++i) {
+    const unsigned n = unit_slots(seq_len(kv, s, i), a.window, TT);
+    mine += n | (n ? 1ll << kCountAt : 0);
+    longest = max(longest, n);
+  }
   long long before = mine;  // inclusive scan over the block
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
     const long long x = __shfl_up_sync(~0u, before, d);
     if (lane >= d) before += x;
   }
-  if (lane == 31) scan[warp] = before;
+  longest = __reduce_max_sync(~0u, longest);
+  if (lane == 31) scan[warp] = make_longlong2(before, longest);
   __syncthreads();
   long long total = 0;
 #pragma unroll
   for (int i = 0; i < kAttMaxWarps; ++i)
     if (i < n_warps) {
-      if (i < warp) before += scan[i];
-      total += scan[i];
+      const longlong2 x = scan[i];
+      if (i < warp) before += x.x;
+      total += x.x;
+      longest = max(longest, (unsigned)x.y);
     }
   before -= mine;
+  const unsigned n_seqs = (unsigned)(total >> kCountAt), seqs_before = (unsigned)(before >> kCountAt);
+  const unsigned seqs_mine = (unsigned)(mine >> kCountAt);
+  constexpr long long kSlotBits = (1ll << kCountAt) - 1;
+  total &= kSlotBits;
+  before &= kSlotBits;
+  mine &= kSlotBits;
+  const unsigned long long slots_all = (unsigned long long)total * a.units;
+  const unsigned long long units_all = (unsigned long long)n_seqs * a.units;
+  // A unit cut between blocks costs their last one a few steps' time, in each
+  // warp.  While blocks of whole units are not longer than that, none is cut.
+  const unsigned long long fair = quotient(slots_all, gridDim.x);
+  const bool by_units = quotient(units_all + gridDim.x - 1, gridDim.x) * longest <= fair + kCutSteps * n_warps;
   // (two slots at least to a block, so that it has a step: the join counts on
   // every block in a row having a part)
-  const unsigned long long slots_all = (unsigned long long)total * a.units;
-  const unsigned blocks = (unsigned)min((unsigned long long)gridDim.x, slots_all / 2);
-  const unsigned long long each = quotient(slots_all, max(blocks, 1u));  // slots of a block; the first `more` have one more
-  const unsigned more = (unsigned)(slots_all - each * blocks);
-  const long long b0 = each * blockIdx.x + min(blockIdx.x, more);
-  const int slots = blockIdx.x < blocks ? (int)each + (blockIdx.x < more) : 0;
+  const unsigned long long items = by_units ? units_all : slots_all;
+  const unsigned blocks = (unsigned)min((unsigned long long)gridDim.x, by_units ? items : items / 2);
+  const unsigned long long each = quotient(items, max(blocks, 1u));  // items of a block; the first `more` have one more
+  const unsigned more = (unsigned)(items - each * blocks);
+  long long b0 = each * blockIdx.x + min(blockIdx.x, more);
+  int slots = blockIdx.x < blocks ? (int)each + (blockIdx.x < more) : 0;
+  if (by_units) {  // from units to slots
+    if (slots > 0 && seqs_mine) {
+#pragma unroll 1
+      for (int end = 0; end < 2; ++end) {
+        long long u = b0 + (end ? slots - 1 : 0) - (long long)seqs_before * a.units;
+        if (u < 0 || u >= (long long)seqs_mine * a.units) continue;
+        long long p = before * a.units;
+#pragma unroll 1
+        for (int i = s0; i < s1; ++i) {
+          const int n = unit_slots(seq_len(kv, s, i), a.window, TT);
+          if (n == 0) continue;
+          if (u < a.units) {
+            from[end] = p + (u + end) * n;  // (the last unit's end)
+            break;
+          }
+          u -= a.units;
+          p += (long long)n * a.units;
+        }
+      }
+    }
+    __syncthreads();
+    b0 = from[0];
+    slots = slots ? (int)(from[1] - b0) : 0;
+    __syncthreads();
+  }
   const int wq = slots / n_warps, wr = slots - wq * n_warps;
   if (mine > 0) {  // whose range starts in this thread's sequences
     const long long lo = before * a.units - b0, hi = lo + mine * a.units;
@@ -1092,15 +1141,14 @@ Variant variant_of(int type, int dim) {
 
 constexpr int kAttStatic = 3584;  // at least what the kernel's static shared memory takes
 
-// Warps and stages: the most warps that leave each 3 stages (2 with more than
-// 8 warps); their first pieces (state_bytes each) stay in shared memory where
+// Warps and stages: the most warps that leave each 2 stages; their first pieces (state_bytes each) stay in shared memory where
 // that costs no warp.
 struct Geometry {
   int warps, stages, first;  // first: its offset in dynamic shared memory (0: in the workspace)
   int smem;
 };
 Geometry geometry(int most, int stage_bytes, int state_bytes) {
-  const int room = kAttSmem - kAttStatic, least = most > 8 ? 2 : 3;
+  const int room = kAttSmem - kAttStatic, least = 2;
   Geometry g;
   g.warps = room / (least * stage_bytes);
   g.warps = g.warps > most ? most : g.warps;
