@@ -36,9 +36,7 @@
 // A operand.  (With the heads as M half of each instruction and of the
 // accumulators would be padding; tcgen05 takes no fewer than 64 rows.)  The
 // weights leave S^T token by token and are needed head by head: one movmatrix
-// per 8 x 8 block turns them.  They enter as two terms, the leading bits and the
-// rest: rounded weights alone would add an error of the size of the result's
-// own rounding.  8-bit codes are multiplied as they are (int8 keys) or become
+// per 8 x 8 block turns them.  8-bit codes are multiplied as they are (int8 keys) or become
 // fp16 exactly, in 3 to 5 instructions per four; K's scales multiply the
 // scores, V's the weights, in fp32.
 //
@@ -838,11 +836,14 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(KvView kv, KvSeqs
             }
           }
       }
-      // The weights times V's scales become fp16 in units such that none
-      // overflows (2^9 over vtop); what is below 2^-33 of the largest is lost.
-      // As two terms: hi keeps the type's leading bits (cut, so that the rest is
-      // exact), lo the rest's.  Each turned: a thread then has two tokens of head g.
-      uint32_t ph[TT][NT][2], pl[TT][NT][2];
+      // bf16: the weights as two terms, hi with the type's leading bits (cut, so
+      // that the rest is exact) and the rest's leading bits: one term would add an
+      // error of the size of the result's own rounding.  8 bits: the weights times
+      // V's scales as fp16, whose 11 bits leave a fraction of that; in units
+      // such that none overflows (2^9 over vtop), what is below 2^-34 of the largest
+      // is lost.  Each turned: a thread then has two tokens of head g.
+      constexpr int TERMS = TYPE == LORA_KV_BF16 ? 2 : 1;
+      uint32_t pw[TERMS][TT][NT][2];
 #pragma unroll
       for (int h = 0; h < NT; ++h) {
         const float base[2] = {m[h][0] == -INFINITY ? 0.f : m[h][0], m[h][1] == -INFINITY ? 0.f : m[h][1]};
@@ -855,16 +856,11 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(KvView kv, KvSeqs
             l[h][1] += p1;
             if (TYPE == LORA_KV_BF16) {
               const uint32_t hi2 = __byte_perm(__float_as_uint(p0), __float_as_uint(p1), 0x7632);
-              ph[t][h][e] = turn(hi2);
-              pl[t][h][e] = turn(pack_bf16x2(p0 - bf16_lo(hi2), p1 - bf16_hi(hi2)));
+              pw[0][t][h][e] = turn(hi2);
+              pw[TERMS - 1][t][h][e] = turn(pack_bf16x2(p0 - bf16_lo(hi2), p1 - bf16_hi(hi2)));
             } else {
               const float w = vs[t][e] * unit;
-              p0 *= w;
-              p1 *= w;
-              const float h0 = __uint_as_float(__float_as_uint(p0) & 0xffffe000u);
-              const float h1 = __uint_as_float(__float_as_uint(p1) & 0xffffe000u);
-              ph[t][h][e] = turn(pack_f16x2(h0, h1));
-              pl[t][h][e] = turn(pack_f16x2(p0 - h0, p1 - h1));
+              pw[0][t][h][e] = turn(pack_f16x2(p0 * w, p1 * w));
             }
           }
       }
@@ -881,8 +877,8 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(KvView kv, KvSeqs
             ldsm4t(v, v32 + (((2 * b + v_c) ^ sw) << 4));
 #pragma unroll
             for (int h = 0; h < NT; ++h) {
-              mma16816(o[h][b], v[0], v[1], v[2], v[3], ph[t][h][0], ph[t][h][1]);
-              mma16816(o[h][b], v[0], v[1], v[2], v[3], pl[t][h][0], pl[t][h][1]);
+              mma16816(o[h][b], v[0], v[1], v[2], v[3], pw[0][t][h][0], pw[0][t][h][1]);
+              mma16816(o[h][b], v[0], v[1], v[2], v[3], pw[TERMS - 1][t][h][0], pw[TERMS - 1][t][h][1]);
             }
           }
         } else {
@@ -899,10 +895,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(KvView kv, KvSeqs
               codes_to_f16<TYPE>(w[2 * x], v0, v1);
               codes_to_f16<TYPE>(w[2 * x + 1], v2, v3);
 #pragma unroll
-              for (int h = 0; h < NT; ++h) {
-                mma_f16(o[h][b], v0, v1, v2, v3, ph[t][h][0], ph[t][h][1]);
-                mma_f16(o[h][b], v0, v1, v2, v3, pl[t][h][0], pl[t][h][1]);
-              }
+              for (int h = 0; h < NT; ++h) mma_f16(o[h][b], v0, v1, v2, v3, pw[0][t][h][0], pw[0][t][h][1]);
             }
           }
         }

@@ -57,11 +57,11 @@ def attend(q, k, v, kv_type, scale, window=0, sinks=None):
 
     With an 8-bit cache q is split into 8-bit terms, which leaves at most 2^-22 of
     a head's largest |q| per dim: within the dim + 4 steps above.  The weights
-    times V's scales are two fp16 terms in units of 2^-9 of the largest scale u (or
-    less): beside the relative error each term may be off by half of fp16's
-    smallest step, 2^-25, so a weight by 2 * 2^-25 * 2^-9 u = 2^-33 u, and the sum
-    over len tokens of codes c by len * 2^-33 u max|c| (weights are relative to one
-    of the scores, so that the denominator is at least 1).
+    times V's scales are rounded to fp16 (2^-11 relative), in units of 2^-9 of the
+    largest scale u (or less): a small one may be off by half of fp16's smallest
+    step, 2^-25 * 2^-9 u = 2^-34 u, and the sum over len tokens of codes c by
+    len * 2^-34 u max|c| (weights are relative to one of the scores, so that the
+    denominator is at least 1).
     """
     heads, dim = q.shape
     kv_heads = k.shape[1]
@@ -78,10 +78,12 @@ def attend(q, k, v, kv_type, scale, window=0, sinks=None):
     out, spread = p @ vx, p @ vx.abs()
     err_s = mag * (dim + 4) * 2.0 ** -23
     rel = 2 * err_s + 2.0 ** -15 + kx.shape[1] * 2.0 ** -23
+    if kv_type != "bf16":
+        rel = rel + 2.0 ** -11
     tol_out = U_BF16 * out.abs() + rel[..., None] * spread * (1 + U_BF16) + 1e-38
     if kv_type != "bf16" and len(v):
         code, u = held(v, kv_type)
-        floor = code.abs().amax((0, 2)) * u.nan_to_num().amax(0) * len(v) * 2.0 ** -33  # [kv_heads]
+        floor = code.abs().amax((0, 2)) * u.nan_to_num().amax(0) * len(v) * 2.0 ** -34  # [kv_heads]
         tol_out = tol_out + floor[:, None, None]
     tol_lse = err_s + (kx.shape[1] + 8) * 2.0 ** -23 + lse.abs().nan_to_num(posinf=0) * 2.0 ** -22
     return out.reshape(heads, dim), lse.reshape(heads), tol_out.reshape(heads, dim), tol_lse.reshape(heads)
