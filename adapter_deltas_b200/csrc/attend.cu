@@ -1110,12 +1110,12 @@ using AttendKernel = void (*)(KvView, KvSeqs, AttendArgs);
 // of a step (a wait, the running maximum) is spread over as many bytes.
 struct Variant {
   AttendKernel kernel[2];  // up to 8 query heads per key head, more
-  int tt, warps;
+  int tt, warps[2];
 };
 
 template <int TYPE, int DIM, bool ANY, int TT, int WARPS>
 Variant variant() {
-  return {{attend_kernel<TYPE, DIM, ANY, TT, WARPS, 1>, attend_kernel<TYPE, DIM, ANY, TT, WARPS, 2>}, TT, WARPS};
+  return {{attend_kernel<TYPE, DIM, ANY, TT, WARPS, 1>, attend_kernel<TYPE, DIM, ANY, TT, 8, 2>}, TT, {WARPS, 8}};
 }
 
 template <int TYPE>
@@ -1199,7 +1199,7 @@ int launch_attend(const lora_kv *kv, int layer, const KvSeqs &s, const AttendCal
   a.scale2 = c.scale * 1.44269504f;
   a.window = c.window;
   const size_t floats = state_floats(a.rows, kv->dim);
-  const Geometry g = geometry(v.warps, v.tt * kv_tile_bytes(kv->type, kv->dim), int(floats * 4));
+  const Geometry g = geometry(v.warps[wide], v.tt * kv_tile_bytes(kv->type, kv->dim), int(floats * 4));
   a.n_stages = g.stages;
   a.first_in_smem = g.first;
   uint8_t *ws = static_cast<uint8_t *>(c.ws);
