@@ -212,6 +212,24 @@ __device__ __forceinline__ Ends finish(const float *sinks, int head, float m, fl
   return e;
 }
 
+// y += w * 8 values of a state (FAR: written by another block, read past L1).
+template <bool FAR = false>
+__device__ __forceinline__ void add8(float (&y)[8], float w, const float4 *p) {
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const float4 z = FAR ? __ldcg(p + k) : p[k];
+    y[4 * k] = fmaf(w, z.x, y[4 * k]);
+    y[4 * k + 1] = fmaf(w, z.y, y[4 * k + 1]);
+    y[4 * k + 2] = fmaf(w, z.z, y[4 * k + 2]);
+    y[4 * k + 3] = fmaf(w, z.w, y[4 * k + 3]);
+  }
+}
+__device__ __forceinline__ void store8(uint8_t *out, const float (&y)[8], float mul) {
+  *reinterpret_cast<uint4 *>(out) =
+      make_uint4(pack_bf16x2(y[0] * mul, y[1] * mul), pack_bf16x2(y[2] * mul, y[3] * mul),
+                 pack_bf16x2(y[4] * mul, y[5] * mul), pack_bf16x2(y[6] * mul, y[7] * mul));
+}
+
 // ------------------------------------------------------------------ kernel
 
 // What a stage of a ring holds (written for the first step of a unit or of a warp's range).
@@ -926,11 +944,12 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(KvView kv, KvSeqs
     }
   }
   __syncthreads();
-  const int quads = dim / 4;
-  const int per_run = a.rows * quads;
+  // a thread has 8 dims of a row
+  const int octs = dim / 8;
+  const int per_run = a.rows * octs;
 #pragma unroll 1
   for (int i0 = tid; i0 < n_runs * per_run && !broken; i0 += blockDim.x) {
-    const int k = i0 / per_run, r = (i0 - k * per_run) / quads, d = (i0 - k * per_run - r * quads) * 4;
+    const int k = i0 / per_run, r = (i0 - k * per_run) / octs, d = (i0 - k * per_run - r * octs) * 8;
     const int f = run[k], e = run[k + 1];
     const int4 p0 = piece[order[f]], p1 = piece[order[e - 1]];
     const bool whole = !(p0.z & 1) && !(p1.z & 2);
@@ -940,34 +959,30 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(KvView kv, KvSeqs
 #pragma unroll 1
     for (int i = f; i < e; ++i) mm = fmaxf(mm, where[order[i]][r]);
     const float bm = mm == -INFINITY ? 0.f : mm;
-    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+    float y[8] = {};
 #pragma unroll 2
     for (int i = f; i < e; ++i) {
       const float *st = where[order[i]];
       const float w = exp2_fast(st[r] - bm);
-      const float4 z = *reinterpret_cast<const float4 *>(st + state_head(a.rows) + r * dim + d);
       ll = fmaf(w, st[a.rows + r], ll);
-      y.x = fmaf(w, z.x, y.x);
-      y.y = fmaf(w, z.y, y.y);
-      y.z = fmaf(w, z.z, y.z);
-      y.w = fmaf(w, z.w, y.w);
+      add8(y, w, reinterpret_cast<const float4 *>(st + state_head(a.rows) + r * dim + d));
     }
     if (whole) {
       const int hd = kvh * a.group + h0 + r;
       const Ends fin = finish(a.sinks, hd, mm, ll);
       if (a.lse && d == 0) a.lse[(long long)p0.x * a.n_heads + hd] = fin.lse;
-      *reinterpret_cast<uint2 *>(a.out + p0.x * a.ldo + ((long long)hd * dim + d) * 2) =
-          make_uint2(pack_bf16x2(y.x * fin.mul, y.y * fin.mul), pack_bf16x2(y.z * fin.mul, y.w * fin.mul));
+      store8(a.out + p0.x * a.ldo + ((long long)hd * dim + d) * 2, y, fin.mul);
     } else {
       float *st = a.part + ((size_t)blockIdx.x * 2 + (p0.z & 1 ? 0 : 1)) * floats;
       if (d == 0) {
         st[r] = mm;
         st[a.rows + r] = ll;
       }
-      *reinterpret_cast<float4 *>(st + state_head(a.rows) + r * dim + d) = y;
+      float4 *to = reinterpret_cast<float4 *>(st + state_head(a.rows) + r * dim + d);
+      to[0] = make_float4(y[0], y[1], y[2], y[3]);
+      to[1] = make_float4(y[4], y[5], y[6], y[7]);
     }
   }
-
   __syncthreads();
 
   // ---- count this block in for the units its borders cut (thread 0: the one it
@@ -1045,32 +1060,21 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(KvView kv, KvSeqs
     }
     __syncthreads();
 #pragma unroll 1
-    for (int x = tid; x < live * quads; x += blockDim.x) {
-      const int r = x / quads, d = (x - r * quads) * 4;
+    for (int x = tid; x < live * octs; x += blockDim.x) {
+      const int r = x / octs, d = (x - r * octs) * 8;
       const float ll = totals[r];
       if (ll < 0.f) continue;  // (a block that gave up: the row stays as it was)
-      const float *at = state(0) + state_head(a.rows) + r * dim + d;
-      float4 y = __ldcg(reinterpret_cast<const float4 *>(at));
-      const float w0 = weight[r];
-      y.x *= w0;
-      y.y *= w0;
-      y.z *= w0;
-      y.w *= w0;
-      at = state(1) + state_head(a.rows) + r * dim + d;
+      float y[8] = {};
+      const size_t at = state_head(a.rows) + r * dim + d;
+      add8<true>(y, weight[r], reinterpret_cast<const float4 *>(state(0) + at));
+      const float *rest = state(1) + at;
 #pragma unroll 4
-      for (int i = 1; i < job.y; ++i) {
-        const float4 z = __ldcg(reinterpret_cast<const float4 *>(at + (size_t)(i - 1) * 2 * floats));
-        const float w = weight[i * a.rows + r];
-        y.x = fmaf(w, z.x, y.x);
-        y.y = fmaf(w, z.y, y.y);
-        y.z = fmaf(w, z.z, y.z);
-        y.w = fmaf(w, z.w, y.w);
-      }
+      for (int i = 1; i < job.y; ++i)
+        add8<true>(y, weight[i * a.rows + r], reinterpret_cast<const float4 *>(rest + (size_t)(i - 1) * 2 * floats));
       const int hd = kvh * a.group + h0 + r;
       const Ends e = finish(a.sinks, hd, tops[r], ll);
       if (a.lse && d == 0) a.lse[(long long)seq * a.n_heads + hd] = e.lse;
-      *reinterpret_cast<uint2 *>(a.out + seq * a.ldo + ((long long)hd * dim + d) * 2) =
-          make_uint2(pack_bf16x2(y.x * e.mul, y.y * e.mul), pack_bf16x2(y.z * e.mul, y.w * e.mul));
+      store8(a.out + seq * a.ldo + ((long long)hd * dim + d) * 2, y, e.mul);
     }
     __syncthreads();
   }
