@@ -110,6 +110,7 @@ _sig("lora_kv_append", _I, [_P, _I, _P, _I, _P, _I, _P, _I, _P, _P, _I, _I, _P])
 _sig("lora_kv_gather", _I, [_P, _I, _P, _I, _P, _I, _P, _I, _P, _P, _I, _I, _P])
 _sig("lora_attend_workspace_bytes", _Z, [_P, _I])
 _sig("lora_attend", _I, [_P, _I, _P, _I, _P, _I, _P, _P, _I, _P, _I, _P, _I, ctypes.c_float, _I, _P, _Z, _P])
+_sig("lora_selftest_stalled_attend", _I, [_P, _I, _P, _I, _P, _I, _I, _P, _I, _P, _I, _P, _Z, _P])
 _sig("lora_rmsnorm", _I, [_I, _P, _I, _P, _I, _P, _I, _P, ctypes.c_float, _P, _I, _P, _I, _P, _I, _I, _I, _P])
 _sig("lora_get_error", _I, [_P, ctypes.POINTER(_I), _P])
 _sig("lora_kernel_launches", ctypes.c_uint64, [])
@@ -535,7 +536,7 @@ def lora_kernel_launches() -> int:
 
 
 def lora_set_wait_limit_ns(ns: int) -> None:
-    """Wall-clock limit of the decode kernel's bounded waits (0: one second)."""
+    """Wall-clock limit of the decode and attention kernels' bounded waits (0: one second)."""
     _lib.lora_set_wait_limit_ns(int(ns))
 
 
@@ -545,3 +546,12 @@ def lora_selftest_stalled_apply(pool: PoolHandle, target: int, x, y, ids, scales
     _check(_lib.lora_selftest_stalled_apply(pool, target, _ptr(x), _ld(x), _ptr(y), _ld(y), _ptr(ids),
                                             _ptr(scales), y.shape[0], _stream(stream)),
            "lora_selftest_stalled_apply")
+
+
+def lora_selftest_stalled_attend(kv: KvHandle, layer: int, q, out, page_table, seq_lens, ws, stream=None) -> None:
+    """Test only: lora_attend with nothing fetched, so that its waits run out
+    (LORA_ERR_TIMEOUT in the cache's sticky status)."""
+    _check(_lib.lora_selftest_stalled_attend(kv, layer, q.data_ptr(), q.stride(0), out.data_ptr(), out.stride(0),
+                                             q.shape[1] // kv.head_dim, page_table.data_ptr(), page_table.shape[1],
+                                             seq_lens.data_ptr(), seq_lens.shape[0], ws.data_ptr(), ws.numel(),
+                                             _stream_on(stream, kv.device)), "lora_selftest_stalled_attend")

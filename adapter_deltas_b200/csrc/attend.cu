@@ -65,6 +65,8 @@ struct AttendArgs {
   float scale2;        // scale * log2(e)
   int window;
   int n_stages;
+  int stall;           // test only: nothing is fetched, so that every wait runs out
+  unsigned long long wait_ns;
   // workspace: what each block's borders cut
   unsigned long long *done;  // [blocks] how many blocks of the unit that starts in a block and goes on are done
   unsigned long long tag;    // of this launch, in done's upper bits: whatever is there from before counts as none
@@ -447,7 +449,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(KvView kv, KvSeqs
       if (TT > 1 && !one_copy) n = __popc(__ballot_sync(~0u, copy));
       if (lane == 0) {
         if (fnew) held[warp][stage] = {fseq, pack_unit(fkvh, fh0), fpos, flen};
-        mbar_arrive_expect_tx(&full[warp][stage], n * tile_bytes);
+        if (!a.stall) mbar_arrive_expect_tx(&full[warp][stage], n * tile_bytes);
       }
       if (n < t1 - t0) {
         const unsigned ok = TT > 1 && !one_copy ? __ballot_sync(~0u, copy) << t0 : 0u;
@@ -455,7 +457,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(KvView kv, KvSeqs
         if (lane == 0) set_status(kv.status, LORA_ERR_BAD_ID);
       }
       __syncwarp();
-      if (copy)
+      if (copy && !a.stall)
         bulk_g2s(ring + stage * stage_bytes + tile * tile_bytes, fhead + at, one_copy ? n * tile_bytes : tile_bytes,
                  &full[warp][stage]);
       fpos += kStep;
@@ -687,10 +689,10 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(KvView kv, KvSeqs
             for (int x = lane * 128; x < bytes; x += 32 * 128) asm volatile("prefetch.global.L1 [%0];" ::"l"(q + x));
         }
       }
-      if (!mbar_wait_bounded(&full[warp][stage], phase, kv.status)) {
+      if (!mbar_wait_bounded(&full[warp][stage], phase, kv.status, a.wait_ns)) {
         // copies in flight must land before the block ends (again a bounded wait)
 #pragma unroll 1
-        for (int k = 0; k < a.n_stages; ++k) (void)mbar_wait_bounded(&full[warp][k], phase ^ (k < stage), kv.status);
+        for (int k = 0; k < a.n_stages; ++k) (void)mbar_wait_bounded(&full[warp][k], phase ^ (k < stage), kv.status, a.wait_ns);
         if (lane == 0) dead_block = 1;
         break;
       }
@@ -1202,6 +1204,8 @@ int launch_attend(const lora_kv *kv, int layer, const KvSeqs &s, const AttendCal
   a.units = kv->heads * a.head_groups;
   a.scale2 = c.scale * 1.44269504f;
   a.window = c.window;
+  a.stall = c.stall;
+  a.wait_ns = wait_limit_ns();
   const size_t floats = state_floats(a.rows, kv->dim);
   const Geometry g = geometry(v.warps[wide], v.tt * kv_tile_bytes(kv->type, kv->dim), int(floats * 4));
   a.n_stages = g.stages;

@@ -511,9 +511,10 @@ struct DecodeCall {
   int stall = 0;  // test only: the producer fills no stage, so every consumer wait runs out
 };
 int launch_decode(lora_pool *pool, const DecodeCall &c, cudaStream_t st);
-// Lowers (ns > 0) or restores (0) the wall-clock limit of the decode
-// kernel's bounded waits; 1 s by default.
+// Lowers (ns > 0) or restores (0) the wall-clock limit of the decode and
+// attention kernels' bounded waits; 1 s by default.
 void set_wait_limit_ns(unsigned long long ns);
+unsigned long long wait_limit_ns();
 // Writes each routed pair's slot (as the in-kernel grouping forms it) to pair_ids.
 int launch_moe_pair_ids(const lora_pool *pool, const int32_t *lora_ids, const int32_t *topk, int n_pairs,
                         int top_k, int n_experts, int32_t *pair_ids, cudaStream_t st);

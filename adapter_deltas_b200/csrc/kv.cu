@@ -342,6 +342,41 @@ KvSeqs seqs_of(const int32_t *table, int max_pages, const int32_t *lens, const i
   return s;
 }
 
+int attend(lora_kv *kv, int layer, const void *q, int ldq, void *out, int ldo, float *lse, const float *sinks, int n_heads,
+           const int32_t *page_table, int max_pages, const int32_t *seq_lens, int n_seqs, float scale, int window, void *ws,
+           size_t ws_bytes, int stall, void *stream) {
+  if (!kv || layer < 0 || layer >= kv->n_layers) return LORA_ERR_INVALID_ARG;
+  if (n_heads < kv->heads || n_heads % kv->heads || n_heads > kKvMaxQHeads) return LORA_ERR_INVALID_ARG;
+  if (n_seqs < 0 || n_seqs > kMaxTokens || max_pages < 0 || window < 0) return LORA_ERR_INVALID_ARG;
+  if (!(scale > 0.f) || scale > 0x1p100f) return LORA_ERR_INVALID_ARG;
+  if (n_seqs == 0) return LORA_OK;
+  if (!q || !out || !page_table || !seq_lens || !ws || max_pages < 1) return LORA_ERR_INVALID_ARG;
+  const int width = n_heads * kv->dim;
+  if (ldq < width || ldo < width) return LORA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(out) || !aligned16(ws) || ldq % 8 || ldo % 8) return LORA_ERR_ALIGNMENT;
+  if ((reinterpret_cast<uintptr_t>(page_table) | reinterpret_cast<uintptr_t>(seq_lens) |
+       reinterpret_cast<uintptr_t>(lse) | reinterpret_cast<uintptr_t>(sinks)) & 3)
+    return LORA_ERR_ALIGNMENT;
+  if (ws_bytes < attend_workspace_bytes(kv, n_heads)) return LORA_ERR_WORKSPACE;
+  if (rows_overlap(q, size_t(ldq) * 2, size_t(width) * 2, n_seqs, out, size_t(ldo) * 2, size_t(width) * 2, n_seqs))
+    return LORA_ERR_INVALID_ARG;
+  AttendCall c;
+  c.q = q;
+  c.ldq = ldq;
+  c.out = out;
+  c.ldo = ldo;
+  c.lse = lse;
+  c.sinks = sinks;
+  c.n_heads = n_heads;
+  c.scale = scale;
+  c.window = window;
+  c.ws = ws;
+  c.stall = stall;
+  DeviceGuard g(kv->device);
+  return launch_attend(kv, layer, seqs_of(page_table, max_pages, seq_lens, nullptr, n_seqs), c,
+                       static_cast<cudaStream_t>(stream));
+}
+
 }  // namespace
 
 extern "C" {
@@ -464,35 +499,16 @@ int lora_attend(lora_kv *kv, int layer, const void *q, int ldq, void *out, int l
                 int n_heads, const int32_t *page_table, int max_pages, const int32_t *seq_lens, int n_seqs, float scale,
                 int window, void *ws, size_t ws_bytes, void *stream) {
   NvtxRange nvtx_range("lora_attend");
-  if (!kv || layer < 0 || layer >= kv->n_layers) return LORA_ERR_INVALID_ARG;
-  if (n_heads < kv->heads || n_heads % kv->heads || n_heads > kKvMaxQHeads) return LORA_ERR_INVALID_ARG;
-  if (n_seqs < 0 || n_seqs > kMaxTokens || max_pages < 0 || window < 0) return LORA_ERR_INVALID_ARG;
-  if (!(scale > 0.f) || scale > 0x1p100f) return LORA_ERR_INVALID_ARG;
-  if (n_seqs == 0) return LORA_OK;
-  if (!q || !out || !page_table || !seq_lens || !ws || max_pages < 1) return LORA_ERR_INVALID_ARG;
-  const int width = n_heads * kv->dim;
-  if (ldq < width || ldo < width) return LORA_ERR_INVALID_ARG;
-  if (!aligned16(q) || !aligned16(out) || !aligned16(ws) || ldq % 8 || ldo % 8) return LORA_ERR_ALIGNMENT;
-  if ((reinterpret_cast<uintptr_t>(page_table) | reinterpret_cast<uintptr_t>(seq_lens) |
-       reinterpret_cast<uintptr_t>(lse) | reinterpret_cast<uintptr_t>(sinks)) & 3)
-    return LORA_ERR_ALIGNMENT;
-  if (ws_bytes < attend_workspace_bytes(kv, n_heads)) return LORA_ERR_WORKSPACE;
-  if (rows_overlap(q, size_t(ldq) * 2, size_t(width) * 2, n_seqs, out, size_t(ldo) * 2, size_t(width) * 2, n_seqs))
-    return LORA_ERR_INVALID_ARG;
-  AttendCall c;
-  c.q = q;
-  c.ldq = ldq;
-  c.out = out;
-  c.ldo = ldo;
-  c.lse = lse;
-  c.sinks = sinks;
-  c.n_heads = n_heads;
-  c.scale = scale;
-  c.window = window;
-  c.ws = ws;
-  DeviceGuard g(kv->device);
-  return launch_attend(kv, layer, seqs_of(page_table, max_pages, seq_lens, nullptr, n_seqs), c,
-                       static_cast<cudaStream_t>(stream));
+  return attend(kv, layer, q, ldq, out, ldo, lse, sinks, n_heads, page_table, max_pages, seq_lens, n_seqs, scale, window,
+                ws, ws_bytes, 0, stream);
+}
+
+int lora_selftest_stalled_attend(lora_kv *kv, int layer, const void *q, int ldq, void *out, int ldo, int n_heads,
+                                 const int32_t *page_table, int max_pages, const int32_t *seq_lens, int n_seqs, void *ws,
+                                 size_t ws_bytes, void *stream) {
+  NvtxRange nvtx_range("lora_selftest_stalled_attend");
+  return attend(kv, layer, q, ldq, out, ldo, nullptr, nullptr, n_heads, page_table, max_pages, seq_lens, n_seqs, 1.f, 0,
+                ws, ws_bytes, 1, stream);
 }
 
 }  // extern "C"

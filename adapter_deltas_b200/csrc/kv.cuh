@@ -210,6 +210,7 @@ struct AttendCall {
   float scale;
   int window;
   void *ws;
+  int stall;  // test only
 };
 int launch_attend(const lora_kv *kv, int layer, const KvSeqs &s, const AttendCall &c, cudaStream_t st);
 size_t attend_workspace_bytes(const lora_kv *kv, int n_heads);

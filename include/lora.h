@@ -697,9 +697,10 @@ LORA_API int lora_get_error(lora_pool *pool, int *device_status, void *stream);
 LORA_API uint64_t lora_kernel_launches(void);
 
 /*
- * Wall-clock limit of the decode kernel's bounded waits (for a stage of its
- * copy ring), in nanoseconds, for the launches that follow; 0 restores the default of one second.  A wait that
- * runs out sets LORA_ERR_TIMEOUT in the pool's sticky status, leaves the
+ * Wall-clock limit of the decode and attention kernels' bounded waits (for a
+ * stage of a copy ring), in nanoseconds, for the launches that follow; 0
+ * restores the default of one second.  A wait that runs out sets
+ * LORA_ERR_TIMEOUT in the pool's (or cache's) sticky status, leaves the
  * rows that needed the data untouched and lets the kernel finish; it never
  * faults.  Tests lower it to reach that path quickly.
  */
@@ -718,6 +719,16 @@ LORA_API void lora_set_wait_limit_ns(uint64_t ns);
 LORA_API int lora_selftest_stalled_apply(lora_pool *pool, int target, const void *x, int ldx,
                                 void *y, int ldy, const int32_t *ids,
                                 const float *scales, int T, void *stream);
+
+/*
+ * The same for lora_attend (scale 1, no window, sinks or lse): nothing is
+ * fetched, every warp's wait runs out, the launch completes, lora_kv_get_error
+ * then reads LORA_ERR_TIMEOUT, rows with tokens are left as they were, and the
+ * cache and the workspace stay usable.
+ */
+LORA_API int lora_selftest_stalled_attend(lora_kv *kv, int layer, const void *q, int ldq, void *out, int ldo, int n_heads,
+                                 const int32_t *page_table, int max_pages, const int32_t *seq_lens, int n_seqs, void *ws,
+                                 size_t ws_bytes, void *stream);
 
 #ifdef __cplusplus
 }

@@ -275,3 +275,24 @@ def test_streams_and_graphs(cuda_device):
             c.b = cut
             check(c, "e4m3", q, out.cpu(), None)
             c.b = whole
+
+
+def test_waits_that_run_out(cuda_device):
+    """Nothing is fetched: the launch completes, says so, leaves the rows, and the next call is right."""
+    b = R.Batch([700, 33, -1, 5, 1200], 2, 64, 16, seed=12)
+    q = queries(b, 8, 12)
+    with Cache(b, "bf16", cuda_device) as c:
+        c.append()
+        ws = torch.full((L.lora_attend_workspace_bytes(c.kv, 8),), 255, dtype=torch.uint8, device=cuda_device)
+        want, _ = attend(c, q, ws=ws)
+        out = torch.full_like(q.to(cuda_device), 7.0)
+        L.lora_set_wait_limit_ns(2_000_000)
+        try:
+            L.lora_selftest_stalled_attend(c.kv, 0, q.to(cuda_device), out, c.table, c.lens, ws)
+            torch.cuda.synchronize()
+        finally:
+            L.lora_set_wait_limit_ns(0)
+        assert c.error() == L.LORA_ERR_TIMEOUT and c.error() == L.LORA_OK
+        assert (out == 7.0).all()
+        got, _ = attend(c, q, ws=ws)
+        assert torch.equal(got, want) and c.error() == L.LORA_OK
