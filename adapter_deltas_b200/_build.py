@@ -12,6 +12,7 @@ binding loads it when LORA_B200_DEBUG=1).
 
 from __future__ import annotations
 
+import concurrent.futures
 import glob
 import os
 import shutil
@@ -51,17 +52,19 @@ def build(force: bool = False, verbose: bool = False, debug: bool = False) -> st
     lib = LIB_DEBUG if debug else LIB
     if not force and not stale(lib):
         return lib
-    objs = []
     build_dir = os.path.join(ROOT, "_build", "debug" if debug else "release")
     os.makedirs(build_dir, exist_ok=True)
-    for src in SOURCES:
+    def compile_one(src: str) -> str:
         obj = os.path.join(build_dir, os.path.basename(src) + ".o")
         cmd = [nvcc(), *NVCC_FLAGS, *(["-DLORA_DEBUG"] if debug else []), "-I", os.path.join(ROOT, "include"),
                "-c", src, "-o", obj]
         if verbose:
             cmd.insert(1, "-Xptxas=-v")
         subprocess.run(cmd, check=True)
-        objs.append(obj)
+        return obj
+
+    with concurrent.futures.ThreadPoolExecutor(max_workers=os.cpu_count() or 1) as pool:
+        objs = list(pool.map(compile_one, SOURCES))
     tmp = lib + ".tmp.%d" % os.getpid()
     subprocess.run([nvcc(), "-gencode", "arch=compute_100a,code=sm_100a", "-shared", "-cudart", "static",
                     "-o", tmp, *objs, "-ldl"], check=True)

@@ -1,1141 +1,16 @@
-// attend.cu -- attention of one new token per sequence over the paged cache.
-//
-// For query head h of sequence s, with key head g = h / (n_heads / heads) and
-// positions j in [max(0, len - window), len):
-//     s_j = scale * q . k_j,   out = sum_j e^(s_j) v_j / (sum_j e^(s_j) + e^sink),
-// in one pass over the cache with a running maximum m and sum l: a step of
-// tokens gives m' = max(m, max s_j), l' = l e^(m - m') + sum e^(s_j - m'), and the
-// weighted values are rescaled by e^(m - m') when the maximum moved (in base
-// 2 throughout: log2(e) is folded into the scale).  Two such states over
-// disjoint tokens join by the same formula, so the tokens can be cut anywhere.
-//
-// Bound by HBM: 4 flops per cached element and query head, at most 16 query
-// heads to a byte.  So the split is by bytes, evenly, whatever the lengths:
-//  - The batch is one flat list of slots, ordered by (sequence, unit, step).  A
-//    unit is one key head with up to 8 (or 16) of its query heads; a step is 16
-//    TT consecutive tokens of it.  A unit has one slot for each step and one
-//    before them for what it costs to begin and end one (about a step's time).
-//    Each block takes an equal range of the list (one block per SM), each of its
-//    warps an equal range of the block's.  Every block finds its place itself from
-//    the lengths (one scan), so there is no plan to keep and nothing of it is read
-//    on the host.
-//  - A warp is on its own: one lane fetches its steps' tiles with bulk copies
-//    (one per 16 tokens: a tile is contiguous in the cache, K, V and scales)
-//    into the warp's ring of stages, several steps ahead, through the page
-//    table; there is no block-wide synchronisation until the end.
-//  - A (sequence, unit) that lies inside one warp's range is written at once.
-//    States of ranges that cut one are joined in the block, in token order;
-//    what a block's border cuts goes to the workspace, and the last of a unit's
-//    blocks to get there joins them (in order again, whichever block it is:
-//    equal inputs give equal bits).  Blocks count themselves in, none waits for
-//    another.  (As a second launch the join took 4 to 6 us.)
-//
-// The products run on the warp-level tensor instruction (m16n8k16): a unit's 8
-// query heads are the N = 8 of both products, S^T = K q^T (16 tokens x 8 heads)
-// and O^T += V^T P^T (16 dims x 8 heads), K and V read from the staged tile as the
-// A operand.  (With the heads as M half of each instruction and of the
-// accumulators would be padding; tcgen05 takes no fewer than 64 rows.)  The
-// weights leave S^T token by token and are needed head by head: one movmatrix
-// per 8 x 8 block turns them.  8-bit codes are multiplied as they are (int8 keys) or become
-// fp16 exactly, in 3 to 5 instructions per four; K's scales multiply the
-// scores, V's the weights, in fp32.
-//
-// Tokens outside the range get weight 0 by selection, not by adding: what lies
-// in their places (the end of a page, before the window) may be anything.
-#include "kv.cuh"
+// attend.cu -- launches of the attention over the paged cache: which variant,
+// how many warps and stages, and where the workspace's parts lie (attend.cuh
+// has the kernel and its reasons).
+#include "attend.cuh"
 
 namespace lora {
 
-constexpr int kAttMaxWarps = 12;
-constexpr int kAttMaxStages = 8;
-constexpr int kAttSmem = 227 * 1024;
-constexpr int kSlack = 4, kVSlack = 2;  // powers of two
-constexpr int kCutSteps = 3;
-
-struct AttendArgs {
-  const uint8_t *q;
-  uint8_t *out;
-  long long ldq, ldo;  // bytes
-  float *lse;
-  const float *sinks;
-  int n_heads, group;  // query heads, and of them per key head
-  int units;           // per sequence: heads * head groups
-  int head_groups;
-  int rows;            // of a state: query heads of a unit (the last unit of a key head may have fewer)
-  float scale2;        // scale * log2(e)
-  int window;
-  int n_stages;
-  int stall;           // test only: nothing is fetched, so that every wait runs out
-  unsigned long long wait_ns;
-  // workspace: what each block's borders cut
-  unsigned long long *done;  // [blocks] how many blocks of the unit that starts in a block and goes on are done
-  unsigned long long tag;    // of this launch, in done's upper bits: whatever is there from before counts as none
-  float *part;         // [blocks][2] states: 0 continues from the block before, 1 starts here
-  float *first;        // [blocks][warps] states: a warp's first piece, when more of its range follows,
-  int first_in_smem;   // or where in shared memory those are (0: not there)
-};
-
-constexpr int kCountBits = 16;  // of done
-
-// A state in memory: m[rows], l[rows] (each row's place a multiple of 16 bytes
-// from the start: rows * 2 rounded up to 4 floats), then rows x dim weighted sums.
-__host__ __device__ constexpr int state_head(int rows) { return (2 * rows + 3) & ~3; }
-__host__ __device__ constexpr int state_floats(int rows, int dim) { return state_head(rows) + rows * dim; }
-
-// ------------------------------------------------------------------ pieces
-
-__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr));
-}
-__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr));
-}
-// 8 x 8 of 16-bit values, transposed: a thread has two neighbours of a row.
-__device__ __forceinline__ uint32_t turn(uint32_t x) {
-  uint32_t r;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
-  return r;
-}
-__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                         uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-__device__ constexpr float exp2_int(int e) { return (float)(1 << e); }
-__device__ __forceinline__ float exp2_fast(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-
-__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                        uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ void mma_s8(int (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                       uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-      : "+r"(c[0]), "+r"(c[1]), "+r"(c[2]), "+r"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
-// Bytes 0 and 2 (even) and 1 and 3 (odd) of a word of codes as fp16 pairs, exactly.
-//  int8: 1024 + (code + 128) is fp16 with the code's bits in its low byte.
-template <int TYPE>
-__device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t &even, uint32_t &odd) {
-  if (TYPE == LORA_KV_E4M3) {
-    const uint32_t x = __byte_perm(w, 0, 0x3120);
-    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
-        : "=r"(even), "=r"(odd)
-        : "r"(x));
-  } else {
-    const uint32_t x = w ^ 0x80808080u;
-    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(even) : "r"(__byte_perm(x, 0x64646464u, 0x4240)), "r"(0x64806480u));
-    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(odd) : "r"(__byte_perm(x, 0x64646464u, 0x4341)), "r"(0x64806480u));
-  }
-}
-
-// A word of K codes as two fp16 pairs: e4m3 bytes 0, 1 and 2, 3 (one instruction
-// each); int8 bytes 0, 2 and 1, 3.
-template <int TYPE>
-__device__ __forceinline__ void key_codes_to_f16(uint32_t w, uint32_t &a, uint32_t &b) {
-  if (TYPE == LORA_KV_E4M3)
-    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
-        : "=r"(a), "=r"(b)
-        : "r"(w));
-  else
-    codes_to_f16<TYPE>(w, a, b);
-}
-
-// How the scores of a unit are formed.
-//  kBf16: q as it is, times bf16 keys.
-//  kF16:  q scaled per head by a power of two to below 2, as fp16: exact down to
-//         2^-14 of the head's largest |q|, below that off by at most 2^-25 of it.
-//         Keys become fp16 exactly.  (The warp-level product of e4m3 operands is
-//         no single instruction of this GPU: it took 1.7 times the instructions
-//         of this form.)
-//  kInt8: q = (hi + lo / 128 + rest / 16384) * amax / 127, all int8: off by at most
-//         2^-22 of the largest |q|.  Keys are multiplied as the codes they are;
-//         products and sums are exact.  (Not for 9 to 16 heads wider than 128: the
-//         three terms would take more registers than there are.)
-enum { kBf16, kF16, kInt8 };
-__host__ __device__ constexpr int score_form(int type, int dim, int nt) {
-  return type == LORA_KV_BF16 ? kBf16 : type == LORA_KV_INT8 && (nt == 1 || dim <= 128) ? kInt8 : kF16;
-}
-__host__ __device__ constexpr int q_regs(int form, int nb, int nt) {  // per n-tile: 6 for two blocks, or 2 a block
-  return nt * (form == kInt8 ? (nb + 1) / 2 * 6 : nb * 2);
-}
-
-// A length that is attended to, else 0 (none, empty, in error).
-__device__ __forceinline__ int valid_len(const KvView &kv, const KvSeqs &s, int len) {
-  return len > 0 && len <= ((long long)s.max_pages << kv.log2_page) ? len : 0;
-}
-__device__ __forceinline__ int seq_len(const KvView &kv, const KvSeqs &s, int i) {
-  return valid_len(kv, s, __ldg(s.lens + i));
-}
-__device__ __forceinline__ int first_token(int len, int window) { return window && len > window ? len - window : 0; }
-// Slots of a unit of a sequence: one, and one for each step of tt tiles (aligned
-// to that) from the first token's to the last one's.  None without a token.
-__device__ __forceinline__ int unit_slots(int len, int window, int tt) {
-  const int per = kTileTokens * tt;
-  return len ? (len + per - 1) / per - first_token(len, window) / per + 1 : 0;
-}
-
-// Write row r's result from its state: o = sums for 4 dims, m and l over all tokens.
-struct Ends {
-  float mul, lse;
-};
-__device__ __forceinline__ Ends finish(const float *sinks, int head, float m, float l) {
-  Ends e;
-  float base = m;
-  if (sinks) {
-    const float sink = sinks[head] * 1.44269504f;
-    base = fmaxf(m, sink);
-    l = l * exp2_fast(m - base) + exp2_fast(sink - base);
-  }
-  e.mul = __fdividef(exp2_fast(m - base), l);
-  if (m == -INFINITY && !sinks) e.mul = __int_as_float(0x7fc00000);  // (every score minus infinity: 0 / 0)
-  e.lse = fmaf(base, 0.693147181f, 0.693147181f * __log2f(l));
-  return e;
-}
-
-// y += w * 8 values of a state (FAR: written by another block, read past L1).
-template <bool FAR = false>
-__device__ __forceinline__ void add8(float (&y)[8], float w, const float4 *p) {
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    const float4 z = FAR ? __ldcg(p + k) : p[k];
-    y[4 * k] = fmaf(w, z.x, y[4 * k]);
-    y[4 * k + 1] = fmaf(w, z.y, y[4 * k + 1]);
-    y[4 * k + 2] = fmaf(w, z.z, y[4 * k + 2]);
-    y[4 * k + 3] = fmaf(w, z.w, y[4 * k + 3]);
-  }
-}
-__device__ __forceinline__ void store8(uint8_t *out, const float (&y)[8], float mul) {
-  *reinterpret_cast<uint4 *>(out) =
-      make_uint4(pack_bf16x2(y[0] * mul, y[1] * mul), pack_bf16x2(y[2] * mul, y[3] * mul),
-                 pack_bf16x2(y[4] * mul, y[5] * mul), pack_bf16x2(y[6] * mul, y[7] * mul));
-}
-
-// ------------------------------------------------------------------ kernel
-
-// What a stage of a ring holds (written for the first step of a unit or of a warp's range).
-struct Step {
-  int seq, unit, pos, len;  // sequence, unit, first token of the step, tokens of the sequence
-};
-// A unit as its key head and the first of its query heads in that head's group, in one number.
-__device__ __forceinline__ int pack_unit(int kvh, int h0) { return kvh << 16 | h0; }
-__device__ __forceinline__ int unit_kvh(int unit) { return unit >> 16; }
-__device__ __forceinline__ int unit_h0(int unit) { return unit & 0xffff; }
-
-// a / b, without the long division where 32 bits do (a call: it is used in places that run once).
-__device__ __noinline__ unsigned long long quotient(unsigned long long a, unsigned long long b) {
-  return (a | b) >> 32 ? a / b : (unsigned)a / (unsigned)b;
-}
-
-// DIM: the head's width, or with ANY the largest of a range of multiples of 16 (kv.dim is the width).
-// TT: tiles of 16 tokens per step.  WARPS: most warps of a block.  NT: 8 NT query heads to a unit.
-template <int TYPE, int DIM, bool ANY, int TT, int WARPS, int NT>
-__global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(KvView kv, KvSeqs s, AttendArgs a) {
-  constexpr int ES = kv_elt(TYPE);
-  constexpr int ROWS = 8 * NT;          // query heads of a unit
-  constexpr int NB = DIM / 16;          // blocks of 16 dims
-  const int dim = ANY ? kv.dim : DIM, nb = ANY ? kv.dim / 16 : NB;
-  const int row_bytes = dim * ES, chunks = row_bytes / 16;
-  constexpr int kStep = kTileTokens * TT;  // tokens of a step
-  const int tile_bytes = kv_tile_bytes(TYPE, dim), stage_bytes = TT * tile_bytes;
-
-  extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ uint64_t full[kAttMaxWarps][kAttMaxStages];
-  __shared__ Step held[kAttMaxWarps][kAttMaxStages];
-  // a warp's first slot, from its sequence's first, and that sequence and its length; last entry: the block's last slot
-  __shared__ longlong2 scan[kAttMaxWarps];
-  __shared__ long long from[kAttMaxWarps + 1];
-  __shared__ int2 start[kAttMaxWarps + 1];
-  __shared__ int4 piece[2 * kAttMaxWarps];  // [2 warp + which]: {sequence (-1: none), unit, cut before 1 / after 2, -}
-  __shared__ const float *where[2 * kAttMaxWarps];
-  __shared__ int order[2 * kAttMaxWarps], run[2 * kAttMaxWarps + 1];  // pieces in order; where each unit's run starts
-  __shared__ int n_runs, dead_block;
-  __shared__ int2 to_join[2];  // {first block, blocks} of units that this block was the last to work on
-
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int n_warps = blockDim.x >> 5;
-  const int floats = state_floats(a.rows, dim);
-
-  if (lane < a.n_stages) mbar_init(&full[warp][lane], 1);
-  fence_mbar_init();
-  if (tid < 2 * kAttMaxWarps) piece[tid] = make_int4(-1, 0, 0, 0);
-  if (tid == 0) dead_block = 0;
-  griddep_wait();
-  griddep_launch_dependents();
-
-  // ---- this block's and this warp's range of the flat list
-  const int per = (s.n + blockDim.x - 1) / blockDim.x;
-  const int s0 = min(s.n, tid * per), s1 = min(s.n, s0 + per);
-  // (slots of a unit, summed, and sequences with a token, counted in the bits above)
-  constexpr int kCountAt = 42;
-  long long mine = 0;
-  unsigned longest = 0;
-#pragma unroll 1
-  for (int i = s0; i < s1; ++i) {
-    const unsigned n = unit_slots(seq_len(kv, s, i), a.window, TT);
-    mine += n | (n ? 1ll << kCountAt : 0);
-    longest = max(longest, n);
-  }
-  long long before = mine;  // inclusive scan over the block
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const long long x = __shfl_up_sync(~0u, before, d);
-    if (lane >= d) before += x;
-  }
-  longest = __reduce_max_sync(~0u, longest);
-  if (lane == 31) scan[warp] = make_longlong2(before, longest);
-  __syncthreads();
-  long long total = 0;
-#pragma unroll
-  for (int i = 0; i < kAttMaxWarps; ++i)
-    if (i < n_warps) {
-      const longlong2 x = scan[i];
-      if (i < warp) before += x.x;
-      total += x.x;
-      longest = max(longest, (unsigned)x.y);
-    }
-  before -= mine;
-  const unsigned n_seqs = (unsigned)(total >> kCountAt), seqs_before = (unsigned)(before >> kCountAt);
-  const unsigned seqs_mine = (unsigned)(mine >> kCountAt);
-  constexpr long long kSlotBits = (1ll << kCountAt) - 1;
-  total &= kSlotBits;
-  before &= kSlotBits;
-  mine &= kSlotBits;
-  const unsigned long long slots_all = (unsigned long long)total * a.units;
-  const unsigned long long units_all = (unsigned long long)n_seqs * a.units;
-  // A unit cut between blocks costs their last one a few steps' time, in each
-  // warp.  While blocks of whole units are not longer than that, none is cut.
-  const unsigned long long fair = quotient(slots_all, gridDim.x);
-  const bool by_units = quotient(units_all + gridDim.x - 1, gridDim.x) * longest <= fair + kCutSteps * n_warps;
-  // (two slots at least to a block, so that it has a step: the join counts on
-  // every block in a row having a part)
-  const unsigned long long items = by_units ? units_all : slots_all;
-  const unsigned blocks = (unsigned)min((unsigned long long)gridDim.x, by_units ? items : items / 2);
-  const unsigned long long each = quotient(items, max(blocks, 1u));  // items of a block; the first `more` have one more
-  const unsigned more = (unsigned)(items - each * blocks);
-  long long b0 = each * blockIdx.x + min(blockIdx.x, more);
-  int slots = blockIdx.x < blocks ? (int)each + (blockIdx.x < more) : 0;
-  if (by_units) {  // from units to slots
-    if (slots > 0 && seqs_mine) {
-#pragma unroll 1
-      for (int end = 0; end < 2; ++end) {
-        long long u = b0 + (end ? slots - 1 : 0) - (long long)seqs_before * a.units;
-        if (u < 0 || u >= (long long)seqs_mine * a.units) continue;
-        long long p = before * a.units;
-#pragma unroll 1
-        for (int i = s0; i < s1; ++i) {
-          const int n = unit_slots(seq_len(kv, s, i), a.window, TT);
-          if (n == 0) continue;
-          if (u < a.units) {
-            from[end] = p + (u + end) * n;  // (the last unit's end)
-            break;
-          }
-          u -= a.units;
-          p += (long long)n * a.units;
-        }
-      }
-    }
-    __syncthreads();
-    b0 = from[0];
-    slots = slots ? (int)(from[1] - b0) : 0;
-    __syncthreads();
-  }
-  const int wq = slots / n_warps, wr = slots - wq * n_warps;
-  if (mine > 0) {  // whose range starts in this thread's sequences
-    const long long lo = before * a.units - b0, hi = lo + mine * a.units;
-    if (lo < slots && hi > 0) {
-#pragma unroll 1
-      for (int w = 0; w <= n_warps; ++w) {
-        const int at = w < n_warps ? wq * w + min(w, wr) : slots - 1;
-        if (at < lo || at >= hi || at >= slots) continue;
-        long long p = lo;
-#pragma unroll 1
-        for (int i = s0; i < s1; ++i) {
-          const int len = seq_len(kv, s, i);
-          const long long e = p + (long long)unit_slots(len, a.window, TT) * a.units;
-          if (at < e) {
-            start[w] = make_int2(i, len);
-            from[w] = at - p;
-            break;
-          }
-          p = e;
-        }
-      }
-    }
-  }
-  __syncthreads();
-  const int count = wq + (warp < wr);  // this warp's slots
-
-  uint8_t *ring = smem + (size_t)warp * a.n_stages * stage_bytes;
-  if (count > 0) {
-    // ---- fetching side: the next step to fetch, and pages of up to 32 tiles
-    int left = count;  // slots not yet passed
-    int fetched = 0;   // steps fetched or being so
-    int fseq = start[warp].x, flen = start[warp].y;
-    int fkvh, fh0, fpos;  // the unit's key head and first query head; first token of the step
-    bool fnew = true;     // the step to fetch is the first of a unit or of the range
-    bool own_slot;        // the unit's own slot is to be passed first
-    {
-      const int n = unit_slots(flen, a.window, TT), unit = (int)quotient(from[warp], n);
-      const int slot = (int)(from[warp] - (long long)unit * n);
-      own_slot = slot == 0;
-      fpos = (first_token(flen, a.window) / kStep + max(slot - 1, 0)) * kStep;
-      fkvh = a.head_groups == 1 ? unit : unit / a.head_groups;
-      fh0 = (unit - fkvh * a.head_groups) * ROWS;
-    }
-    const bool starts_inside = fpos > first_token(flen, a.window);  // of its unit
-    unsigned bad_tiles = 0;     // bits stage * TT ..: tiles of a stage that are on no page of the cache
-    const long long head_stride = kv_head_stride(kv);
-    const uint8_t *fhead = kv.base + fkvh * head_stride;
-    // a step's tiles lie in one page, one behind the other, unless pages are shorter
-    const bool one_copy = TT == 1 || (1 << kv.log2_page) >= kStep;
-    // lane i: page of the sequence's tile base + i, or -1
-    auto load_pages = [&](int seq, int len, int base) {
-      const int tok = (base + lane) * kTileTokens;
-      return tok < len ? __ldg(s.table + (long long)seq * s.max_pages + (tok >> kv.log2_page)) : -1;
-    };
-    int pbase = fpos / kTileTokens & ~31, pages = load_pages(fseq, flen, pbase);
-    // the sequence after: its length is read when this one begins, its first pages when this one's last unit does
-    int nlen = fseq + 1 < s.n ? __ldg(s.lens + fseq + 1) : 0, npages = 0;
-    auto load_next = [&]() {
-      if (fkvh != kv.heads - 1 || fh0 + ROWS < a.group || fseq + 1 >= s.n) return;
-      nlen = valid_len(kv, s, nlen);
-      npages = load_pages(fseq + 1, nlen, first_token(nlen, a.window) / kStep * TT & ~31);
-    };
-    load_next();
-
-    auto fetch = [&](int stage) {
-      if (own_slot) {
-        --left;
-        own_slot = false;
-      }
-      if (left <= 0) return;
-      --left;
-      ++fetched;
-      const int t = fpos / kTileTokens;
-      if ((t & ~31) != pbase) {
-        pbase = t & ~31;
-        pages = load_pages(fseq, flen, pbase);
-      }
-      // tiles [t0, t1) of the step, by lane 0 in one copy or by a lane each
-      const int t0 = max(first_token(flen, a.window) / kTileTokens - t, 0);
-      const int t1 = min((flen - fpos + kTileTokens - 1) / kTileTokens, TT);
-      const int tile = one_copy ? t0 : t0 + lane;
-      const int page = __shfl_sync(~0u, pages, (t + tile) & 31);
-      const long long at = kv_tile_offset(kv, page, fpos + tile * kTileTokens);
-      bool copy = at >= 0 && lane < (one_copy ? 1 : t1 - t0);
-      int n = at >= 0 ? t1 - t0 : 0;
-      if (TT > 1 && !one_copy) n = __popc(__ballot_sync(~0u, copy));
-      if (lane == 0) {
-        if (fnew) held[warp][stage] = {fseq, pack_unit(fkvh, fh0), fpos, flen};
-        if (!a.stall) mbar_arrive_expect_tx(&full[warp][stage], n * tile_bytes);
-      }
-      if (n < t1 - t0) {
-        const unsigned ok = TT > 1 && !one_copy ? __ballot_sync(~0u, copy) << t0 : 0u;
-        bad_tiles |= (((1u << t1) - (1u << t0)) & ~ok) << (stage * TT);
-        if (lane == 0) set_status(kv.status, LORA_ERR_BAD_ID);
-      }
-      __syncwarp();
-      if (copy && !a.stall)
-        bulk_g2s(ring + stage * stage_bytes + tile * tile_bytes, fhead + at, one_copy ? n * tile_bytes : tile_bytes,
-                 &full[warp][stage]);
-      fpos += kStep;
-      fnew = fpos >= flen;
-      if (fnew) {
-        own_slot = true;
-        fh0 += ROWS;
-        if (fh0 >= a.group) {
-          fh0 = 0;
-          ++fkvh;
-          fhead += head_stride;
-        }
-        if (fkvh == kv.heads) {
-          fkvh = 0;
-          fhead = kv.base;
-          if (left > 1) {  // (another step is to come)
-            ++fseq;
-            flen = valid_len(kv, s, nlen);
-            pages = npages;
-            pbase = first_token(flen, a.window) / kStep * TT & ~31;
-#pragma unroll 1
-            while (flen == 0) {
-              ++fseq;
-              flen = seq_len(kv, s, fseq);
-              pbase = -1;
-            }
-            nlen = fseq + 1 < s.n ? __ldg(s.lens + fseq + 1) : 0;
-          }
-        }
-        fpos = first_token(flen, a.window) / kStep * kStep;
-        load_next();
-      }
-    };
-
-    // ---- computing side
-    const uint32_t ring32 = smem_u32(ring);
-    const int g = lane >> 2, j2 = 2 * (lane & 3);  // of a product: its row (token, dim) and its pair of columns (heads)
-    const int r8 = lane & 7, mat = lane >> 3;      // this lane's row and matrix of an ldmatrix
-    const int low = chunks & -chunks, grp = low < 8 ? low : 8;
-    const int sw = (r8 / (8 / grp)) & (grp - 1);  // its rows' chunk permutation (rows r8 and r8 + 8 share it)
-    // K: (tokens 0-7 | 8-15) x (chunk | next chunk); V, transposed: the same for 8 bits, for bf16 chunks first
-    const uint32_t k_row = ((mat & 1) * 8 + r8) * row_bytes;
-    const uint32_t v_row = (kTileTokens + (TYPE == LORA_KV_BF16 ? mat >> 1 : mat & 1) * 8 + r8) * row_bytes;
-    const int k_c = mat >> 1, v_c = TYPE == LORA_KV_BF16 ? mat & 1 : mat >> 1;
-
-    constexpr int FORM = score_form(TYPE, DIM, NT);
-    constexpr int QN = q_regs(FORM, NB, 1);
-    uint32_t qa[NT][QN];
-    float qs[NT][2];  // what a score is multiplied by: the softmax's scale and that of q's terms
-    float o[NT][NB][4], m[NT][2], l[NT][2];
-    float vtop = 0.f, unit = 0.f;  // (8 bits) V's scales: reference, and the weights' unit by it
-    int cseq = -1, cunit = -1, cpos = 0, clen = 0, cfirst = 0;  // of the step to compute; cfirst: the unit's first token
-    bool cut_before = false, cnew = true;
-    int stage = 0, fstage = 0;
-    uint32_t phase = 0;
-
-    // q as the products' B operand: columns = heads, rows = dims in the order of the K operand
-    auto load_q = [&]() {
-      const int kvh = unit_kvh(cunit), h0 = unit_h0(cunit), j = lane & 3;
-#pragma unroll
-      for (int h = 0; h < NT; ++h) {
-        const bool live = h0 + g + 8 * h < a.group;
-        const uint8_t *q = a.q + cseq * a.ldq + (long long)(kvh * a.group + h0 + g + 8 * h) * dim * 2;
-        uint2 u[NB];  // bf16: dims 16 b + 2 j, + 1, + 8, + 9; 8 bits: dims 16 b + 4 j ..
-#pragma unroll
-        for (int b = 0; b < NB; ++b) {
-          u[b] = make_uint2(0, 0);
-          if (!live || (ANY && b >= nb)) continue;
-          if (TYPE == LORA_KV_BF16) {
-            u[b].x = __ldg(reinterpret_cast<const uint32_t *>(q + b * 32 + j * 4));
-            u[b].y = __ldg(reinterpret_cast<const uint32_t *>(q + b * 32 + j * 4 + 16));
-          } else {
-            u[b] = __ldg(reinterpret_cast<const uint2 *>(q + b * 32 + j * 8));
-          }
-        }
-        if (FORM == kBf16) {
-          qs[h][0] = qs[h][1] = a.scale2;
-#pragma unroll
-          for (int b = 0; b < NB; ++b) {
-            qa[h][b * 2] = u[b].x;
-            qa[h][b * 2 + 1] = u[b].y;
-          }
-          continue;
-        }
-        uint32_t top = 0;  // bits of the head's largest |q|
-#pragma unroll
-        for (int b = 0; b < NB; ++b)
-          top = max(top, max(max(u[b].x & 0x7fffu, (u[b].x >> 16) & 0x7fffu), max(u[b].y & 0x7fffu, (u[b].y >> 16) & 0x7fffu)));
-        top = max(top, __shfl_xor_sync(~0u, top, 1));
-        top = max(top, __shfl_xor_sync(~0u, top, 2));
-        const float amax = fmaxf(__uint_as_float(top << 16), 0x1p-100f);  // (a NaN is lost here and comes back below)
-        const float two = __uint_as_float(__float_as_uint(amax) & 0x7f800000u);  // 2^E, 2^E <= amax
-        const float mul = FORM == kInt8 ? 127.f / amax : 1.f / two;
-        float mine = FORM == kInt8 ? amax * (1.f / (127.f * 16384.f)) : two;
-        mine = top >= 0x7f80u ? __int_as_float(0x7fc00000) : mine * a.scale2;
-        qs[h][0] = __shfl_sync(~0u, mine, 4 * j2);
-        qs[h][1] = __shfl_sync(~0u, mine, 4 * j2 + 4);
-#pragma unroll
-        for (int b = 0; b < NB; ++b) {
-          float x[4] = {bf16_lo(u[b].x) * mul, bf16_hi(u[b].x) * mul, bf16_lo(u[b].y) * mul, bf16_hi(u[b].y) * mul};
-          if (FORM == kInt8) {
-#pragma unroll
-            for (int k = 0; k < 3; ++k) {  // adding 1.5 * 2^23 rounds to an integer, in the sum's low bits
-              float y[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e) y[e] = x[e] + 12582912.f;
-              const uint32_t lo = __byte_perm(__float_as_uint(y[0]), __float_as_uint(y[1]), 0x0040);
-              const uint32_t hi = __byte_perm(__float_as_uint(y[2]), __float_as_uint(y[3]), 0x0040);
-              qa[h][(b >> 1) * 6 + 2 * k + (b & 1)] = __byte_perm(lo, hi, 0x5410);
-#pragma unroll
-              for (int e = 0; e < 4; ++e) x[e] = (x[e] - (y[e] - 12582912.f)) * 128.f;
-            }
-          } else {  // as key_codes_to_f16 pairs the dims
-            qa[h][b * 2] = TYPE == LORA_KV_E4M3 ? pack_f16x2(x[0], x[1]) : pack_f16x2(x[0], x[2]);
-            qa[h][b * 2 + 1] = TYPE == LORA_KV_E4M3 ? pack_f16x2(x[2], x[3]) : pack_f16x2(x[1], x[3]);
-          }
-        }
-      }
-    };
-
-    // (the first iterations fill the ring: one place in the code for each part)
-#pragma unroll 1
-    for (int i = 1 - a.n_stages;; ++i) {
-      asm volatile("" : "+r"(i));  // (one copy of the loop's body, not one for the filling)
-      fetch(fstage);
-      if (++fstage == a.n_stages) fstage = 0;
-      if (i < 0) continue;
-      int leaving = i == fetched ? 2 : cnew;  // (opaque, for the same reason)
-      asm volatile("" : "+r"(leaving));
-      if (leaving) {
-        if (cseq >= 0) {
-          // The unit's state leaves the registers: as its result when the warp
-          // has seen all of it, else as a piece to be joined (at the range's end
-          // the ring is free for it).
-          const bool cut_after = leaving == 2 && !cnew;
-          const bool whole = !cut_before && !cut_after;
-          const int kvh = unit_kvh(cunit), h0 = unit_h0(cunit);
-          float *state = leaving == 2 ? reinterpret_cast<float *>(ring) : a.first_in_smem
-                             ? reinterpret_cast<float *>(smem + a.first_in_smem) + warp * floats
-                             : a.first + ((size_t)blockIdx.x * kAttMaxWarps + warp) * floats;
-          if (!whole && lane == 0) {
-            const int k = 2 * warp + (cut_before ? 0 : 1);
-            piece[k] = make_int4(cseq, cunit, (cut_before ? 1 : 0) | (cut_after ? 2 : 0), 0);
-            where[k] = state;
-          }
-#pragma unroll
-          for (int h = 0; h < NT; ++h) {
-            float mul[2];
-            bool on[2];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              l[h][e] += __shfl_xor_sync(~0u, l[h][e], 4);
-              l[h][e] += __shfl_xor_sync(~0u, l[h][e], 8);
-              l[h][e] += __shfl_xor_sync(~0u, l[h][e], 16);
-              const int r = 8 * h + j2 + e, hd = kvh * a.group + h0 + r;
-              on[e] = r < a.rows && h0 + r < a.group;
-              mul[e] = TYPE == LORA_KV_BF16 ? 1.f : vtop / exp2_int(15 - kSlack - kVSlack);
-              if (!on[e]) continue;
-              if (whole) {
-                const Ends x = finish(a.sinks, hd, m[h][e], l[h][e]);
-                mul[e] *= x.mul;
-                if (a.lse && g == 0) a.lse[(long long)cseq * a.n_heads + hd] = x.lse;
-              } else if (g == 0) {
-                state[r] = m[h][e];
-                state[a.rows + r] = l[h][e];
-              }
-            }
-            const int r = 8 * h + j2;
-            float *sums = state + state_head(a.rows) + r * dim;
-            uint8_t *out = a.out + cseq * a.ldo + (long long)(kvh * a.group + h0 + r) * dim * 2;
-            // a thread's two neighbouring dims of each of its two heads; 8 bits:
-            // rows g and g + 8 are dims 2 g and 2 g + 1; bf16: dims g and g + 8, and
-            // neighbouring rows trade one
-            const int d0 = TYPE != LORA_KV_BF16 ? 2 * g : g & 1 ? 7 + g : g;
-            auto pair_of = [&](int b, int e) {
-              float2 x = make_float2(o[h][b][e], o[h][b][2 + e]);
-              if (TYPE == LORA_KV_BF16) {
-                const float got = __shfl_xor_sync(~0u, g & 1 ? x.x : x.y, 4);
-                x = g & 1 ? make_float2(got, x.y) : make_float2(x.x, got);
-              }
-              return make_float2(x.x * mul[e], x.y * mul[e]);
-            };
-            if (whole) {
-#pragma unroll
-              for (int b = 0; b < NB; ++b)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                  if (ANY && b >= nb) continue;
-                  const float2 x = pair_of(b, e);
-                  if (on[e]) *reinterpret_cast<uint32_t *>(out + (e * dim + 16 * b + d0) * 2) = pack_bf16x2(x.x, x.y);
-                }
-            } else {
-#pragma unroll
-              for (int b = 0; b < NB; ++b)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                  if (ANY && b >= nb) continue;
-                  const float2 x = pair_of(b, e);
-                  if (on[e]) *reinterpret_cast<float2 *>(sums + e * dim + 16 * b + d0) = x;
-                }
-            }
-          }
-        }
-        if (leaving == 2) break;
-        cut_before = i == 0 && starts_inside;
-        const Step st = held[warp][stage];
-        cseq = st.seq;
-        cunit = st.unit;
-        cpos = st.pos;
-        clen = st.len;
-        cfirst = first_token(clen, a.window);
-#pragma unroll
-        for (int h = 0; h < NT; ++h) {
-          m[h][0] = m[h][1] = -INFINITY;
-          l[h][0] = l[h][1] = 0.f;
-#pragma unroll
-          for (int b = 0; b < NB; ++b) o[h][b][0] = o[h][b][1] = o[h][b][2] = o[h][b][3] = 0.f;
-        }
-        vtop = unit = 0.f;
-        load_q();
-        {  // the next unit's q, towards this SM: the rows behind, or the next sequence's first
-          const int kvh = unit_kvh(cunit), h0 = unit_h0(cunit);
-          const bool last = kvh == kv.heads - 1 && h0 + ROWS >= a.group;
-          const uint8_t *q = last ? a.q + (cseq + 1) * a.ldq
-                                  : a.q + cseq * a.ldq + (long long)(kvh * a.group + min(h0 + ROWS, a.group)) * dim * 2;
-          const int bytes = a.rows * dim * 2;
-          if (!last || cseq + 1 < s.n)
-#pragma unroll 1
-            for (int x = lane * 128; x < bytes; x += 32 * 128) asm volatile("prefetch.global.L1 [%0];" ::"l"(q + x));
-        }
-      }
-      if (!mbar_wait_bounded(&full[warp][stage], phase, kv.status, a.wait_ns)) {
-        // copies in flight must land before the block ends (again a bounded wait)
-#pragma unroll 1
-        for (int k = 0; k < a.n_stages; ++k) (void)mbar_wait_bounded(&full[warp][k], phase ^ (k < stage), kv.status, a.wait_ns);
-        if (lane == 0) dead_block = 1;
-        break;
-      }
-      const uint32_t st32 = ring32 + stage * stage_bytes;
-      uint8_t *stp = ring + stage * stage_bytes;
-      // tokens of the step that count: [lo, hi) of its 16 TT, without those on bad pages
-      const int lo = cfirst - cpos, hi = clen - cpos;
-      const unsigned bad = bad_tiles >> (stage * TT) & ((1u << TT) - 1u);
-      const bool partial = lo > 0 || hi < kStep || bad;
-      bad_tiles &= ~(((1u << TT) - 1u) << (stage * TT));
-      cpos += kStep;
-      cnew = cpos >= clen;
-      if (TYPE != LORA_KV_INT8 && partial) {
-        // weight 0 times what lies there must be 0: clear V's rows outside (int8 has no NaN)
-#pragma unroll 1
-        for (int x = lane; x < kStep * chunks; x += 32) {
-          const int t = x / chunks;
-          if (t >= lo && t < hi && !(bad >> (t / kTileTokens) & 1)) continue;
-          *reinterpret_cast<uint4 *>(stp + (t / kTileTokens) * tile_bytes + (kTileTokens + t % kTileTokens) * row_bytes +
-                                     (x - t * chunks) * 16) = make_uint4(0, 0, 0, 0);
-        }
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncwarp();
-      }
-
-      // ---- scores: [16 TT tokens] x [heads]; rows g and g + 8 of each tile, columns j2 and j2 + 1
-      float c[TT][NT][4];
-#pragma unroll
-      for (int t = 0; t < TT; ++t) {
-        const uint32_t k32 = st32 + t * tile_bytes + k_row;
-        float d[NT][4] = {};  // a second sum for the odd blocks: a shorter chain
-        int ci[3][NT][4] = {};
-#pragma unroll
-        for (int h = 0; h < NT; ++h) c[t][h][0] = c[t][h][1] = c[t][h][2] = c[t][h][3] = 0.f;
-        if (FORM == kBf16) {
-#pragma unroll
-          for (int b = 0; b < NB; ++b) {
-            if (ANY && b >= nb) continue;
-            uint32_t k[4];
-            ldsm4(k, k32 + (((2 * b + k_c) ^ sw) << 4));
-#pragma unroll
-            for (int h = 0; h < NT; ++h)
-              mma16816(b & 1 ? d[h] : c[t][h], k[0], k[1], k[2], k[3], qa[h][2 * b], qa[h][2 * b + 1]);
-          }
-        } else {
-#pragma unroll
-          for (int p = 0; p < (NB + 1) / 2; ++p) {
-            if (ANY && 2 * p >= nb) continue;
-            uint32_t w[4];  // (tokens 0-7 | 8-15) x (block 2p | 2p + 1)
-            ldsm4(w, k32 + (((2 * p + k_c) ^ sw) << 4));
-            if (FORM == kInt8) {  // (past the row's end q's terms are 0 and any code will do)
-#pragma unroll
-              for (int h = 0; h < NT; ++h)
-#pragma unroll
-                for (int k = 0; k < 3; ++k)
-                  mma_s8(ci[k][h], w[0], w[1], w[2], w[3], qa[h][p * 6 + 2 * k], qa[h][p * 6 + 2 * k + 1]);
-            } else {
-#pragma unroll
-              for (int x = 0; x < 2; ++x) {
-                const int b = 2 * p + x;
-                if (b >= NB || (ANY && b >= nb)) continue;
-                uint32_t k0, k1, k2, k3;
-                key_codes_to_f16<TYPE>(w[2 * x], k0, k2);
-                key_codes_to_f16<TYPE>(w[2 * x + 1], k1, k3);
-#pragma unroll
-                for (int h = 0; h < NT; ++h) mma_f16(x ? d[h] : c[t][h], k0, k1, k2, k3, qa[h][2 * b], qa[h][2 * b + 1]);
-              }
-            }
-          }
-        }
-        float ks[2] = {1.f, 1.f};
-        if (TYPE != LORA_KV_BF16) {
-          const uint8_t *sc = stp + t * tile_bytes + 2 * kTileTokens * row_bytes;
-          ks[0] = *reinterpret_cast<const float *>(sc + g * 4);
-          ks[1] = *reinterpret_cast<const float *>(sc + g * 4 + 32);
-        }
-#pragma unroll
-        for (int h = 0; h < NT; ++h)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            if (FORM == kInt8)
-              c[t][h][e] = fmaf((float)(ci[0][h][e] * 128 + ci[1][h][e]), 128.f, (float)ci[2][h][e]);
-            else
-              c[t][h][e] += d[h][e];
-            c[t][h][e] *= TYPE == LORA_KV_BF16 ? qs[h][e & 1] : ks[e >> 1] * qs[h][e & 1];
-          }
-      }
-
-      // ---- weights
-      float vs[TT][2];
-      if (TYPE != LORA_KV_BF16) {
-#pragma unroll
-        for (int t = 0; t < TT; ++t) {
-          const uint8_t *sc = stp + t * tile_bytes + 2 * kTileTokens * row_bytes + kTileTokens * 4;
-          vs[t][0] = *reinterpret_cast<const float *>(sc + g * 4);
-          vs[t][1] = *reinterpret_cast<const float *>(sc + g * 4 + 32);
-        }
-      }
-      if (partial) {
-#pragma unroll
-        for (int t = 0; t < TT; ++t)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int j = t * kTileTokens + g + 8 * e;
-            if (j < lo || j >= hi || (bad >> t & 1)) {
-#pragma unroll
-              for (int h = 0; h < NT; ++h) c[t][h][2 * e] = c[t][h][2 * e + 1] = -INFINITY;
-              if (TYPE != LORA_KV_BF16) vs[t][e] = 0.f;
-            }
-          }
-      }
-      // m is a reference, within 2^kSlack of the running maximum: while no
-      // score passes it by more, nothing is exchanged and nothing rescaled.
-      // V's scales likewise have vtop, within 2^kVSlack of the largest so far.
-      float mx[NT][2], vm = 0.f;
-      bool moved = false;
-#pragma unroll
-      for (int h = 0; h < NT; ++h)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          mx[h][e] = c[0][h][e];
-#pragma unroll
-          for (int t = 0; t < TT; ++t) mx[h][e] = fmaxf(mx[h][e], fmaxf(c[t][h][e], c[t][h][e + 2]));
-          moved |= mx[h][e] > m[h][e] + kSlack;
-        }
-      if (TYPE != LORA_KV_BF16) {
-#pragma unroll
-        for (int t = 0; t < TT; ++t) vm = fmaxf(vm, fmaxf(vs[t][0], vs[t][1]));
-        moved |= vm > vtop * (1 << kVSlack);
-      }
-      if (__any_sync(~0u, moved)) {
-        float fade = 1.f;
-        if (TYPE != LORA_KV_BF16) {
-          vm = fmaxf(vm, __shfl_xor_sync(~0u, vm, 4));
-          vm = fmaxf(vm, __shfl_xor_sync(~0u, vm, 8));
-          vm = fmaxf(vm, __shfl_xor_sync(~0u, vm, 16));
-          if (vm > vtop) {
-            fade = __fdividef(vtop, vm);
-            vtop = vm;
-            unit = exp2_int(15 - kSlack - kVSlack) / vtop;
-          }
-        }
-#pragma unroll
-        for (int h = 0; h < NT; ++h)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float x = mx[h][e];
-            x = fmaxf(x, __shfl_xor_sync(~0u, x, 4));
-            x = fmaxf(x, __shfl_xor_sync(~0u, x, 8));
-            x = fmaxf(x, __shfl_xor_sync(~0u, x, 16));
-            x = fmaxf(x, m[h][e]);
-            float alpha = exp2_fast(m[h][e] - (x == -INFINITY ? 0.f : x));
-            l[h][e] *= alpha;
-            m[h][e] = x;
-            alpha *= fade;
-#pragma unroll
-            for (int b = 0; b < NB; ++b) {
-              if (ANY && b >= nb) continue;
-              o[h][b][e] *= alpha;
-              o[h][b][e + 2] *= alpha;
-            }
-          }
-      }
-      // bf16: the weights as two terms, hi with the type's leading bits (cut, so
-      // that the rest is exact) and the rest's leading bits: one term would add an
-      // error of the size of the result's own rounding.  8 bits: the weights times
-      // V's scales as fp16, whose 11 bits leave a fraction of that; in units
-      // such that none overflows (2^9 over vtop), what is below 2^-34 of the largest
-      // is lost.  Each turned: a thread then has two tokens of head g.
-      constexpr int TERMS = TYPE == LORA_KV_BF16 ? 2 : 1;
-      uint32_t pw[TERMS][TT][NT][2];
-#pragma unroll
-      for (int h = 0; h < NT; ++h) {
-        const float base[2] = {m[h][0] == -INFINITY ? 0.f : m[h][0], m[h][1] == -INFINITY ? 0.f : m[h][1]};
-#pragma unroll
-        for (int t = 0; t < TT; ++t)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {  // tokens g and g + 8
-            float p0 = exp2_fast(c[t][h][2 * e] - base[0]), p1 = exp2_fast(c[t][h][2 * e + 1] - base[1]);
-            l[h][0] += p0;
-            l[h][1] += p1;
-            if (TYPE == LORA_KV_BF16) {
-              const uint32_t hi2 = __byte_perm(__float_as_uint(p0), __float_as_uint(p1), 0x7632);
-              pw[0][t][h][e] = turn(hi2);
-              pw[TERMS - 1][t][h][e] = turn(pack_bf16x2(p0 - bf16_lo(hi2), p1 - bf16_hi(hi2)));
-            } else {
-              const float w = vs[t][e] * unit;
-              pw[0][t][h][e] = turn(pack_f16x2(p0 * w, p1 * w));
-            }
-          }
-      }
-
-      // ---- weighted values: [16 dims] x [heads]
-#pragma unroll
-      for (int t = 0; t < TT; ++t) {
-        const uint32_t v32 = st32 + t * tile_bytes + v_row;
-        if (TYPE == LORA_KV_BF16) {
-#pragma unroll
-          for (int b = 0; b < NB; ++b) {
-            if (ANY && b >= nb) continue;
-            uint32_t v[4];
-            ldsm4t(v, v32 + (((2 * b + v_c) ^ sw) << 4));
-#pragma unroll
-            for (int h = 0; h < NT; ++h) {
-              mma16816(o[h][b], v[0], v[1], v[2], v[3], pw[0][t][h][0], pw[0][t][h][1]);
-              mma16816(o[h][b], v[0], v[1], v[2], v[3], pw[TERMS - 1][t][h][0], pw[TERMS - 1][t][h][1]);
-            }
-          }
-        } else {
-#pragma unroll
-          for (int p = 0; p < (NB + 1) / 2; ++p) {
-            if (ANY && 2 * p >= nb) continue;
-            uint32_t w[4];
-            ldsm4t(w, v32 + (((2 * p + v_c) ^ sw) << 4));
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              const int b = 2 * p + x;
-              if (b >= NB || (ANY && b >= nb)) continue;
-              uint32_t v0, v1, v2, v3;  // even and odd dims of tokens 0-7, then of 8-15
-              codes_to_f16<TYPE>(w[2 * x], v0, v1);
-              codes_to_f16<TYPE>(w[2 * x + 1], v2, v3);
-#pragma unroll
-              for (int h = 0; h < NT; ++h) mma_f16(o[h][b], v0, v1, v2, v3, pw[0][t][h][0], pw[0][t][h][1]);
-            }
-          }
-        }
-      }
-      __syncwarp();  // (all lanes have read the stage)
-      if (++stage == a.n_stages) {
-        stage = 0;
-        phase ^= 1;
-      }
-    }
-  }
-  __syncthreads();
-
-  // ---- join what the warps' borders cut: pieces of one unit follow one another
-  const bool broken = dead_block != 0;
-  if (warp == 0) {
-    const int4 p = lane < 2 * n_warps ? piece[lane] : make_int4(-1, 0, 0, 0);
-    const unsigned there = __ballot_sync(~0u, p.x >= 0), below = there & ((1u << lane) - 1u);
-    const int prev = below ? 31 - __clz(below) : lane;
-    const int px = __shfl_sync(~0u, p.x, prev), pu = __shfl_sync(~0u, p.y, prev);
-    const bool first = p.x >= 0 && (!below || px != p.x || pu != p.y);
-    const unsigned firsts = __ballot_sync(~0u, first);
-    if (p.x >= 0) order[__popc(below)] = lane;
-    if (first) run[__popc(firsts & ((1u << lane) - 1u))] = __popc(below);
-    if (lane == 0) {
-      n_runs = __popc(firsts);
-      run[__popc(firsts)] = __popc(there);
-    }
-  }
-  __syncthreads();
-  // a thread has 8 dims of a row
-  const int octs = dim / 8;
-  const int per_run = a.rows * octs;
-#pragma unroll 1
-  for (int i0 = tid; i0 < n_runs * per_run && !broken; i0 += blockDim.x) {
-    const int k = i0 / per_run, r = (i0 - k * per_run) / octs, d = (i0 - k * per_run - r * octs) * 8;
-    const int f = run[k], e = run[k + 1];
-    const int4 p0 = piece[order[f]], p1 = piece[order[e - 1]];
-    const bool whole = !(p0.z & 1) && !(p1.z & 2);
-    const int kvh = unit_kvh(p0.y), h0 = unit_h0(p0.y);
-    if (h0 + r >= a.group) continue;
-    float mm = -INFINITY, ll = 0.f;
-#pragma unroll 1
-    for (int i = f; i < e; ++i) mm = fmaxf(mm, where[order[i]][r]);
-    const float bm = mm == -INFINITY ? 0.f : mm;
-    float y[8] = {};
-#pragma unroll 2
-    for (int i = f; i < e; ++i) {
-      const float *st = where[order[i]];
-      const float w = exp2_fast(st[r] - bm);
-      ll = fmaf(w, st[a.rows + r], ll);
-      add8(y, w, reinterpret_cast<const float4 *>(st + state_head(a.rows) + r * dim + d));
-    }
-    if (whole) {
-      const int hd = kvh * a.group + h0 + r;
-      const Ends fin = finish(a.sinks, hd, mm, ll);
-      if (a.lse && d == 0) a.lse[(long long)p0.x * a.n_heads + hd] = fin.lse;
-      store8(a.out + p0.x * a.ldo + ((long long)hd * dim + d) * 2, y, fin.mul);
-    } else {
-      float *st = a.part + ((size_t)blockIdx.x * 2 + (p0.z & 1 ? 0 : 1)) * floats;
-      if (d == 0) {
-        st[r] = mm;
-        st[a.rows + r] = ll;
-      }
-      float4 *to = reinterpret_cast<float4 *>(st + state_head(a.rows) + r * dim + d);
-      to[0] = make_float4(y[0], y[1], y[2], y[3]);
-      to[1] = make_float4(y[4], y[5], y[6], y[7]);
-    }
-  }
-  __syncthreads();
-
-  // ---- count this block in for the units its borders cut (thread 0: the one it
-  // begins in, thread 32: the one it ends in); the last of a unit's blocks joins
-  if (tid == 0 || tid == 32) {
-    const int which = tid >> 5;
-    to_join[which] = make_int2(0, 0);
-    if (slots > 0) {
-      const int at = which ? n_warps : 0;
-      const int n = unit_slots(start[at].y, a.window, TT);
-      const int in = (int)(from[at] - quotient(from[at], n) * n);  // slot of its unit
-      // the unit's first and last step's slots in the list
-      const long long here = which ? b0 + slots - 1 : b0, s_first = here - in + 1, s_last = here - in + n - 1;
-      const bool cut = which ? in > 0 && s_last > here && s_first >= b0 : in > 1;
-      if (cut) {
-        auto block_of = [&](unsigned long long slot) {
-          const unsigned long long big = (each + 1) * more;
-          return (int)(slot < big ? quotient(slot, each + 1) : more + quotient(slot - big, each));
-        };
-        const int b_first = block_of(s_first), b_last = block_of(s_last);
-        if (broken)  // (no result for what this block was to add to)
-#pragma unroll 1
-          for (int r = 0; r < a.rows; ++r) a.part[((size_t)blockIdx.x * 2 + which) * floats + a.rows + r] = -1.f;
-        __threadfence();
-        unsigned long long seen = atomicAdd(a.done + b_first, 0ull), next;
-        do {
-          next = (seen >> kCountBits) == a.tag ? seen + 1 : a.tag << kCountBits | 1;
-          const unsigned long long was = atomicCAS(a.done + b_first, seen, next);
-          if (was == seen) break;
-          seen = was;
-        } while (true);
-        __threadfence();
-        if ((int)(next & ((1u << kCountBits) - 1u)) == b_last - b_first + 1) {
-          a.done[b_first] = 0;
-          to_join[which] = make_int2(b_first, b_last - b_first + 1);
-        }
-      }
-    }
-  }
-  __syncthreads();
-#pragma unroll 1
-  for (int which = 0; which < 2; ++which) {
-    const int2 job = to_join[which];
-    if (!job.y) continue;
-    const int unit = which ? n_warps : 0, seq = start[unit].x;
-    const int un = (int)quotient(from[unit], unit_slots(start[unit].y, a.window, TT));
-    const int kvh = un / a.head_groups, h0 = (un - kvh * a.head_groups) * ROWS, live = min(a.rows, a.group - h0);
-    // the first block's own part (1), then those after it (0)
-    auto state = [&](int i) { return a.part + ((size_t)(job.x + i) * 2 + (i ? 0 : 1)) * floats; };
-    float *weight = reinterpret_cast<float *>(smem);  // [parts][rows], behind it [rows] maxima and sums (the rings are idle)
-    float *tops = weight + job.y * a.rows, *totals = tops + a.rows;
-#pragma unroll 1
-    for (int r = warp; r < live; r += n_warps) {
-      float mm = -INFINITY, ll = 0.f;
-      bool none = false;
-#pragma unroll 1
-      for (int i = lane; i < job.y; i += 32) {
-        mm = fmaxf(mm, __ldcg(state(i) + r));
-        none |= __ldcg(state(i) + a.rows + r) < 0.f;
-      }
-      for (int d = 16; d; d >>= 1) mm = fmaxf(mm, __shfl_xor_sync(~0u, mm, d));
-      const float bm = mm == -INFINITY ? 0.f : mm;
-#pragma unroll 1
-      for (int i = lane; i < job.y; i += 32) {
-        const float w = exp2_fast(__ldcg(state(i) + r) - bm);
-        weight[i * a.rows + r] = w;
-        ll = fmaf(w, __ldcg(state(i) + a.rows + r), ll);
-      }
-      for (int d = 16; d; d >>= 1) ll += __shfl_xor_sync(~0u, ll, d);
-      if (__any_sync(~0u, none)) ll = -1.f;
-      if (lane == 0) {
-        tops[r] = mm;
-        totals[r] = ll;
-      }
-    }
-    __syncthreads();
-#pragma unroll 1
-    for (int x = tid; x < live * octs; x += blockDim.x) {
-      const int r = x / octs, d = (x - r * octs) * 8;
-      const float ll = totals[r];
-      if (ll < 0.f) continue;  // (a block that gave up: the row stays as it was)
-      float y[8] = {};
-      const size_t at = state_head(a.rows) + r * dim + d;
-      add8<true>(y, weight[r], reinterpret_cast<const float4 *>(state(0) + at));
-      const float *rest = state(1) + at;
-#pragma unroll 4
-      for (int i = 1; i < job.y; ++i)
-        add8<true>(y, weight[i * a.rows + r], reinterpret_cast<const float4 *>(rest + (size_t)(i - 1) * 2 * floats));
-      const int hd = kvh * a.group + h0 + r;
-      const Ends e = finish(a.sinks, hd, tops[r], ll);
-      if (a.lse && d == 0) a.lse[(long long)seq * a.n_heads + hd] = e.lse;
-      store8(a.out + seq * a.ldo + ((long long)hd * dim + d) * 2, y, e.mul);
-    }
-    __syncthreads();
-  }
-
-  // ---- sequences without a token: zeros, or untouched (length -1, and lengths in error)
-#pragma unroll 1
-  for (int i0 = blockIdx.x + warp * 32 * gridDim.x; i0 < s.n; i0 += gridDim.x * blockDim.x) {
-    const int i = i0 + lane * gridDim.x;
-    int len = 1;
-    if (i < s.n) {
-      len = __ldg(s.lens + i);
-      if (len < -1 || len > ((long long)s.max_pages << kv.log2_page)) set_status(kv.status, LORA_ERR_BAD_ID);
-    }
-    unsigned empty = __ballot_sync(~0u, len == 0);
-    while (empty) {
-      const int z = __ffs(empty) - 1;
-      empty &= empty - 1;
-      const int q = i0 + z * gridDim.x;
-#pragma unroll 1
-      for (int c = lane; c < a.n_heads * dim / 8; c += 32)
-        *reinterpret_cast<uint4 *>(a.out + q * a.ldo + c * 16) = make_uint4(0, 0, 0, 0);
-      if (a.lse)
-#pragma unroll 1
-        for (int h = lane; h < a.n_heads; h += 32)
-          a.lse[(long long)q * a.n_heads + h] = a.sinks ? a.sinks[h] : -INFINITY;
-    }
-  }
-}
-
-// ------------------------------------------------------------------ host
-
 namespace {
 
-using AttendKernel = void (*)(KvView, KvSeqs, AttendArgs);
-
-// Steps of about 8 KiB: several tiles where a tile is small, so that the cost
-// of a step (a wait, the running maximum) is spread over as many bytes.
-struct Variant {
-  AttendKernel kernel[2];  // up to 8 query heads per key head, more
-  int tt, warps[2];
-};
-
-template <int TYPE, int DIM, bool ANY, int TT, int WARPS>
-Variant variant() {
-  return {{attend_kernel<TYPE, DIM, ANY, TT, WARPS, 1>, attend_kernel<TYPE, DIM, ANY, TT, 8, 2>}, TT, {WARPS, 8}};
-}
-
-template <int TYPE>
-Variant variant_of(int dim) {
-  constexpr int W = TYPE == LORA_KV_BF16 ? 1 : 2, N = TYPE == LORA_KV_BF16 ? 8 : 12;
-  if (dim == 64) return variant<TYPE, 64, false, 2 * W, N>();
-  if (dim == 128) return variant<TYPE, 128, false, W, N>();
-  if (dim == 256) return variant<TYPE, 256, false, 1, 8>();
-  return dim < 128 ? variant<TYPE, 128, true, W, N>() : variant<TYPE, 256, true, 1, 8>();
-}
 Variant variant_of(int type, int dim) {
-  return type == LORA_KV_BF16   ? variant_of<LORA_KV_BF16>(dim)
-         : type == LORA_KV_E4M3 ? variant_of<LORA_KV_E4M3>(dim)
-                                : variant_of<LORA_KV_INT8>(dim);
+  return type == LORA_KV_BF16   ? attend_variant_bf16(dim)
+         : type == LORA_KV_E4M3 ? attend_variant_e4m3(dim)
+                                : attend_variant_int8(dim);
 }
 
 constexpr int kAttStatic = 3584;  // at least what the kernel's static shared memory takes
