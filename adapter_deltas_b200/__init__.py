@@ -398,7 +398,7 @@ def _rows(t, name: str, device: int, width: int, dtype, where: str):
             (stride[1] != 1 and width > 1):
         raise ValueError("%s: %s must be %s [T, %d] with unit column stride on cuda:%d, not %s %s %s"
                          % (where, name, dtype, width, device, t.dtype, tuple(shape), t.device))
-    return t.data_ptr(), stride[0] if shape[0] > 1 else max(stride[0], (width + 7) // 8 * 8)
+    return t.data_ptr(), stride[0] if shape[0] > 1 else (width + 7) // 8 * 8
 
 
 def _dense(t, name: str, device: int, shape, dtype, where: str) -> int:

@@ -39,7 +39,7 @@ Geometry geometry(int most, int stage_bytes, int state_bytes) {
 // workspace holds from another use does not look like one.
 unsigned long long next_tag() {
   static std::atomic<uint64_t> n{1};
-  return n.fetch_add(1) * 0x9e3779b97f4aull % ((1ull << 48) - 1) + 1;
+  return n.fetch_add(1) * 0x9e3779b97f4aull % ((1ull << 48) - 2) + 1;
 }
 
 int group_of(const lora_kv *kv, int n_heads) { return n_heads / kv->heads; }

@@ -185,7 +185,7 @@ __host__ __device__ constexpr int q_regs(int form, int nb, int nt) {  // per n-t
 
 // A length that is attended to, else 0 (none, empty, in error).
 __device__ __forceinline__ int valid_len(const KvView &kv, const KvSeqs &s, int len) {
-  return len > 0 && len <= ((long long)s.max_pages << kv.log2_page) ? len : 0;
+  return len > 0 && kv_len_ok(kv, s, len) ? len : 0;
 }
 __device__ __forceinline__ int seq_len(const KvView &kv, const KvSeqs &s, int i) {
   return valid_len(kv, s, __ldg(s.lens + i));
@@ -682,10 +682,10 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(KvView kv, KvSeqs
         load_q();
         {  // the next unit's q, towards this SM: the rows behind, or the next sequence's first
           const int kvh = unit_kvh(cunit), h0 = unit_h0(cunit);
-          const bool last = kvh == kv.heads - 1 && h0 + ROWS >= a.group;
+          const bool more_heads = h0 + ROWS < a.group, last = kvh == kv.heads - 1 && !more_heads;
           const uint8_t *q = last ? a.q + (cseq + 1) * a.ldq
                                   : a.q + cseq * a.ldq + (long long)(kvh * a.group + min(h0 + ROWS, a.group)) * dim * 2;
-          const int bytes = a.rows * dim * 2;
+          const int bytes = (more_heads ? min(a.rows, a.group - h0 - ROWS) : a.rows) * dim * 2;
           if (!last || cseq + 1 < s.n)
 #pragma unroll 1
             for (int x = lane * 128; x < bytes; x += 32 * 128) asm volatile("prefetch.global.L1 [%0];" ::"l"(q + x));
@@ -1090,7 +1090,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(KvView kv, KvSeqs
     int len = 1;
     if (i < s.n) {
       len = __ldg(s.lens + i);
-      if (len < -1 || len > ((long long)s.max_pages << kv.log2_page)) set_status(kv.status, LORA_ERR_BAD_ID);
+      if (len < -1 || !kv_len_ok(kv, s, len)) set_status(kv.status, LORA_ERR_BAD_ID);
     }
     unsigned empty = __ballot_sync(~0u, len == 0);
     while (empty) {

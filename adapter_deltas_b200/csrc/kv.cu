@@ -85,7 +85,7 @@ __device__ __forceinline__ void locate_rows(const KvView &kv, const KvSeqs &s, i
       const int len = s.lens[seq];
       const bool none = len == -1 || (len == 0 && !s.offsets);
       if (!none) {
-        if (len > 0 && len <= ((long long)s.max_pages << kv.log2_page) && own <= len) {
+        if (len > 0 && kv_len_ok(kv, s, len) && own <= len) {
           const int pos = len - back;
           at = kv_tile_offset(kv, s.table[(long long)seq * s.max_pages + (pos >> kv.log2_page)], pos);
           row = pos & (kTileTokens - 1);

@@ -57,6 +57,12 @@ struct KvSeqs {
   int n;
 };
 
+// A length that the table has room for, and that leaves positions room in 32 bits.
+constexpr int kKvMaxLen = 1 << 30;
+__device__ __forceinline__ bool kv_len_ok(const KvView &kv, const KvSeqs &s, int len) {
+  return len <= kKvMaxLen && len <= ((long long)s.max_pages << kv.log2_page);
+}
+
 // Byte offset of a token's tile of head 0 from the layer's base, -1 where the
 // page number is not one of the cache's.
 __device__ __forceinline__ long long kv_tile_offset(const KvView &kv, int page, int pos) {

@@ -591,7 +591,7 @@ LORA_API int lora_kv_get_error(lora_kv *kv, int *device_status, void *stream);
  *                its tokens p * page_tokens ..; entries that hold no token of
  *                the call are not read
  *   seq_lens     device int32 [n_seqs]: each sequence's length with the call's
- *                tokens included; -1 (or 0) = no request in this place
+ *                tokens included, at most 2^30; -1 (or 0) = no request here
  *   row_offsets  device int32 [n_seqs + 1], not decreasing, inside [0, T]: rows
  *                row_offsets[s] .. row_offsets[s + 1] - 1 are the last tokens of
  *                sequence s (none, one or many).  NULL: T == n_seqs and row s is

@@ -296,3 +296,56 @@ def test_waits_that_run_out(cuda_device):
         assert (out == 7.0).all()
         got, _ = attend(c, q, ws=ws)
         assert torch.equal(got, want) and c.error() == L.LORA_OK
+
+
+@pytest.mark.parametrize("seed", range(10))
+def test_random_batches(cuda_device, seed):
+    """Lengths, head layouts and windows at random: every way of cutting a batch into blocks, warps and pieces."""
+    g = torch.Generator().manual_seed(100 + seed)
+    pick = lambda *v: v[int(torch.randint(len(v), (1,), generator=g))]  # noqa: E731
+    kv_type = pick(*R.TYPES)
+    kv_heads, group, dim = pick(1, 2, 3, 8), pick(1, 2, 4, 7, 8, 9, 16, 20), pick(16, 32, 64, 128, 144, 256)
+    most = pick(20, 200, 3000)
+    lens = (torch.rand(pick(1, 3, 40, 150), generator=g) ** 3 * most).int().tolist()
+    for i in range(0, len(lens), 7):
+        lens[i] = pick(-1, 0, lens[i], most)
+    window, page = pick(0, 0, 1, 50, 300), pick(16, 32, 256)
+    b = R.Batch(lens, kv_heads, dim, page, seed=seed)
+    q = queries(b, kv_heads * group, seed)
+    sinks = torch.randn(kv_heads * group, generator=g) if pick(True, False) else None
+    with Cache(b, kv_type, cuda_device) as c:
+        c.append()
+        check(c, kv_type, q, *attend(c, q, window=window, sinks=sinks), window=window, sinks=sinks)
+
+
+def test_one_workspace_for_caches_and_graphs_in_turn(cuda_device):
+    """Calls that follow one another may share a workspace: two caches of different shapes, each in its graph."""
+    batches = [R.Batch([1500, 3, 700], 2, 64, 16, seed=13), R.Batch([900, 900], 1, 128, 32, seed=14)]
+    caches = [Cache(b, t, cuda_device) for b, t in zip(batches, ("int8", "bf16"))]
+    try:
+        qs = [queries(b, h, 13) for b, h in zip(batches, (8, 12))]
+        size = max(L.lora_attend_workspace_bytes(c.kv, h) for c, h in zip(caches, (8, 12)))
+        ws = torch.full((size,), 255, dtype=torch.uint8, device=cuda_device)
+        graphs, outs = [], []
+        for c, q in zip(caches, qs):
+            c.append()
+            qd, out = q.to(cuda_device), torch.zeros_like(q, device=cuda_device)
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph):
+                L.lora_attend(c.kv, 0, qd, out, c.table, c.lens, ws)
+            graphs.append((graph, qd)), outs.append(out)
+        want = [attend(c, q)[0] for c, q in zip(caches, qs)]
+        for turn in range(6):
+            for out in outs:
+                out.zero_()
+            for graph, _ in graphs if turn % 2 else graphs[::-1]:
+                graph.replay()
+            if turn == 3:
+                ws.random_(0, 255)  # whatever is written there in between does not matter
+            torch.cuda.synchronize()
+            assert all(torch.equal(o.cpu(), w) for o, w in zip(outs, want))
+        for c, t, q, out in zip(caches, ("int8", "bf16"), qs, outs):
+            check(c, t, q, out.cpu(), None)
+    finally:
+        for c in caches:
+            c.__exit__()
