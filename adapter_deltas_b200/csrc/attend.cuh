@@ -317,19 +317,48 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(KvView kv, KvSeqs
       total += x.x;
       longest = max(longest, (unsigned)x.y);
     }
-  before -= mine;
-  const unsigned n_seqs = (unsigned)(total >> kCountAt), seqs_before = (unsigned)(before >> kCountAt);
-  const unsigned seqs_mine = (unsigned)(mine >> kCountAt);
   constexpr long long kSlotBits = (1ll << kCountAt) - 1;
-  total &= kSlotBits;
-  before &= kSlotBits;
-  mine &= kSlotBits;
-  const unsigned long long slots_all = (unsigned long long)total * a.units;
-  const unsigned long long units_all = (unsigned long long)n_seqs * a.units;
+  long long *prefix = reinterpret_cast<long long *>(smem);  // [threads], before the rings are in use
+  prefix[tid] = before - mine;
+  __syncthreads();
+
+  // The sequence at place y of the list of slots (or of sequences with a token),
+  // by a whole warp: the last thread whose share starts at or before y, then its
+  // sequences.  before: the slots in front of it.
+  auto find = [&](long long y, bool by_count, int &seq, int &len, long long &before) {
+    auto key = [&](long long x) { return by_count ? x >> kCountAt : x & kSlotBits; };
+    int t = __popc(__ballot_sync(~0u, key(prefix[lane * n_warps]) <= y)) - 1;
+    t = t * n_warps + __popc(__ballot_sync(~0u, lane < n_warps && key(prefix[min(t * n_warps + lane, (int)blockDim.x - 1)]) <= y)) - 1;
+    long long sum = prefix[t];
+    const int end = min(s.n, (t + 1) * per);
+#pragma unroll 1
+    for (int i0 = t * per; i0 < end; i0 += 32) {
+      const int l = i0 + lane < end ? seq_len(kv, s, i0 + lane) : 0;
+      const unsigned n = unit_slots(l, a.window, TT);
+      const long long own = n | (n ? 1ll << kCountAt : 0);
+      long long upto = own;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const long long x = __shfl_up_sync(~0u, upto, d);
+        if (lane >= d) upto += x;
+      }
+      const unsigned past = __ballot_sync(~0u, key(sum + upto) > y);
+      if (past) {
+        const int at = __ffs(past) - 1;
+        seq = i0 + at;
+        len = __shfl_sync(~0u, l, at);
+        before = __shfl_sync(~0u, (sum + upto - own) & kSlotBits, at);
+        return;
+      }
+      sum += __shfl_sync(~0u, upto, 31);
+    }
+  };
+
+  const unsigned long long slots_all = (unsigned long long)(total & kSlotBits) * a.units;
+  const unsigned long long units_all = (unsigned long long)(total >> kCountAt) * a.units;
   // A unit cut between blocks costs their last one a few steps' time, in each
   // warp.  While blocks of whole units are not longer than that, none is cut.
-  const unsigned long long fair = quotient(slots_all, gridDim.x);
-  const bool by_units = quotient(units_all + gridDim.x - 1, gridDim.x) * longest <= fair + kCutSteps * n_warps;
+  const bool by_units = (units_all + gridDim.x - 1) * longest <= slots_all + (unsigned long long)kCutSteps * n_warps * gridDim.x;
   // (two slots at least to a block, so that it has a step: the join counts on
   // every block in a row having a part)
   const unsigned long long items = by_units ? units_all : slots_all;
@@ -338,25 +367,13 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(KvView kv, KvSeqs
   const unsigned more = (unsigned)(items - each * blocks);
   long long b0 = each * blockIdx.x + min(blockIdx.x, more);
   int slots = blockIdx.x < blocks ? (int)each + (blockIdx.x < more) : 0;
-  if (by_units) {  // from units to slots
-    if (slots > 0 && seqs_mine) {
-#pragma unroll 1
-      for (int end = 0; end < 2; ++end) {
-        long long u = b0 + (end ? slots - 1 : 0) - (long long)seqs_before * a.units;
-        if (u < 0 || u >= (long long)seqs_mine * a.units) continue;
-        long long p = before * a.units;
-#pragma unroll 1
-        for (int i = s0; i < s1; ++i) {
-          const int n = unit_slots(seq_len(kv, s, i), a.window, TT);
-          if (n == 0) continue;
-          if (u < a.units) {
-            from[end] = p + (u + end) * n;  // (the last unit's end)
-            break;
-          }
-          u -= a.units;
-          p += (long long)n * a.units;
-        }
-      }
+  if (by_units) {  // from units to slots: warp 0 the first unit's start, warp 1 the last one's end
+    if (slots > 0 && warp < 2) {
+      const long long u = warp ? b0 + slots - 1 : b0, y = quotient(u, a.units);
+      int seq = 0, len = 0;
+      long long p = 0;
+      find(y, true, seq, len, p);
+      if (lane == 0) from[warp] = p * a.units + (u - y * a.units + warp) * unit_slots(len, a.window, TT);
     }
     __syncthreads();
     b0 = from[0];
@@ -364,28 +381,20 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(KvView kv, KvSeqs
     __syncthreads();
   }
   const int wq = slots / n_warps, wr = slots - wq * n_warps;
-  if (mine > 0) {  // whose range starts in this thread's sequences
-    const long long lo = before * a.units - b0, hi = lo + mine * a.units;
-    if (lo < slots && hi > 0) {
 #pragma unroll 1
-      for (int w = 0; w <= n_warps; ++w) {
-        const int at = w < n_warps ? wq * w + min(w, wr) : slots - 1;
-        if (at < lo || at >= hi || at >= slots) continue;
-        long long p = lo;
-#pragma unroll 1
-        for (int i = s0; i < s1; ++i) {
-          const int len = seq_len(kv, s, i);
-          const long long e = p + (long long)unit_slots(len, a.window, TT) * a.units;
-          if (at < e) {
-            start[w] = make_int2(i, len);
-            from[w] = at - p;
-            break;
-          }
-          p = e;
-        }
-      }
+  for (int w = warp; w <= n_warps; w += n_warps) {  // this warp's first slot; warp 0: the block's last one too
+    const int at = w < n_warps ? wq * w + min(w, wr) : slots - 1;
+    if (at >= slots || at < 0) continue;
+    const long long x = b0 + at, y = quotient(x, a.units);
+    int seq = 0, len = 0;
+    long long p = 0;
+    find(y, false, seq, len, p);
+    if (lane == 0) {
+      start[w] = make_int2(seq, len);
+      from[w] = x - p * a.units;
     }
   }
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // (prefix, before the copies into the rings)
   __syncthreads();
   const int count = wq + (warp < wr);  // this warp's slots
 
