@@ -391,13 +391,14 @@ class KvHandle:
 # microseconds on the GPU: their checks read each property of a tensor once.
 
 
-def _rows(t, name: str, device: int, width: int, dtype, where: str):
+def _rows(t, name: str, device: int, width: int, dtype, where: str, rows: Optional[int] = None):
     """Address and leading dimension of a [T, ld] operand whose rows of `width` values are reached by its row stride."""
     shape, stride = t.shape, t.stride()
     if t.dtype is not dtype or t.get_device() != device or len(shape) != 2 or shape[1] != width or \
-            (stride[1] != 1 and width > 1):
-        raise ValueError("%s: %s must be %s [T, %d] with unit column stride on cuda:%d, not %s %s %s"
-                         % (where, name, dtype, width, device, t.dtype, tuple(shape), t.device))
+            (stride[1] != 1 and width > 1) or (rows is not None and shape[0] != rows):
+        raise ValueError("%s: %s must be %s [%s, %d] with unit column stride on cuda:%d, not %s %s %s"
+                         % (where, name, dtype, "T" if rows is None else rows, width, device, t.dtype, tuple(shape),
+                            t.device))
     return t.data_ptr(), stride[0] if shape[0] > 1 else (width + 7) // 8 * 8
 
 
@@ -447,10 +448,10 @@ def lora_kv_get_error(kv: KvHandle, stream=None) -> int:
 def _kv_rows(fn, where: str, kv: KvHandle, layer: int, k, v, page_table, seq_lens, row_offsets, stream) -> None:
     import torch
     dev, width, T, n = kv.device, kv.n_kv_heads * kv.head_dim, k.shape[0], seq_lens.shape[0]
-    if v.shape[0] != T or page_table.dim() != 2:
-        raise ValueError("%s: k and v must have the same rows, page_table [n_seqs, max_pages]" % where)
+    if page_table.dim() != 2:
+        raise ValueError("%s: page_table must be [n_seqs, max_pages]" % where)
     kp, ldk = _rows(k, "k", dev, width, torch.bfloat16, where)
-    vp, ldv = _rows(v, "v", dev, width, torch.bfloat16, where)
+    vp, ldv = _rows(v, "v", dev, width, torch.bfloat16, where, T)
     table = _dense(page_table, "page_table", dev, (n, page_table.shape[1]), torch.int32, where)
     lens = _dense(seq_lens, "seq_lens", dev, (n,), torch.int32, where)
     off = None if row_offsets is None else _dense(row_offsets, "row_offsets", dev, (n + 1,), torch.int32, where)
@@ -480,10 +481,10 @@ def lora_attend(kv: KvHandle, layer: int, q, out, page_table, seq_lens, ws, scal
     import torch
     dev, n, width = kv.device, seq_lens.shape[0], q.shape[-1]
     where, n_heads = "lora_attend", width // kv.head_dim
-    if width % kv.head_dim or q.shape[0] != n or out.shape[0] != n or page_table.dim() != 2:
-        raise ValueError("%s: q and out must be [n_seqs, n_heads * head_dim], page_table [n_seqs, max_pages]" % where)
-    qp, ldq = _rows(q, "q", dev, width, torch.bfloat16, where)
-    op, ldo = _rows(out, "out", dev, width, torch.bfloat16, where)
+    if width % kv.head_dim or page_table.dim() != 2:
+        raise ValueError("%s: q must be [n_seqs, n_heads * head_dim], page_table [n_seqs, max_pages]" % where)
+    qp, ldq = _rows(q, "q", dev, width, torch.bfloat16, where, n)
+    op, ldo = _rows(out, "out", dev, width, torch.bfloat16, where, n)
     table = _dense(page_table, "page_table", dev, (n, page_table.shape[1]), torch.int32, where)
     lens = _dense(seq_lens, "seq_lens", dev, (n,), torch.int32, where)
     sp = None if sinks is None else _dense(sinks, "sinks", dev, (n_heads,), torch.float32, where)
@@ -502,13 +503,16 @@ def lora_rmsnorm(x, weight, eps: float, residual=None, residual_out=None, y=None
     where, dev, (T, d), bf16 = "lora_rmsnorm", x.get_device(), x.shape, torch.bfloat16
     xp, ldx = _rows(x, "x", dev, d, bf16, where)
     wp = _dense(weight, "weight", dev, (d,), bf16, where)
-    ptr, ld = [None] * 4, [0] * 4
-    for i, (t, name, kind) in enumerate(((residual, "residual", bf16), (residual_out, "residual_out", bf16),
-                                         (y, "y", bf16), (q, "q", torch.float8_e4m3fn))):
-        if t is not None:
-            if t.shape[0] != T:
-                raise ValueError("%s: %s must have x's %d rows" % (where, name, T))
-            ptr[i], ld[i] = _rows(t, name, dev, d, kind, where)
+    rp = op = yp = qp = None
+    ldr = ldo = ldy = ldq = 0
+    if residual is not None:
+        rp, ldr = _rows(residual, "residual", dev, d, bf16, where, T)
+    if residual_out is not None:
+        op, ldo = _rows(residual_out, "residual_out", dev, d, bf16, where, T)
+    if y is not None:
+        yp, ldy = _rows(y, "y", dev, d, bf16, where, T)
+    if q is not None:
+        qp, ldq = _rows(q, "q", dev, d, torch.float8_e4m3fn, where, T)
     group, sp = 0, None
     if q is not None:
         if q_scales is None:
@@ -517,12 +521,12 @@ def lora_rmsnorm(x, weight, eps: float, residual=None, residual_out=None, y=None
             n = q_scales.shape[1]
             if n < 1 or d % n:
                 raise ValueError("%s: q_scales must be [T] or [T, d / group]" % where)
-            group = d // n
+            group = d // n if n > 1 else 0
             sp = _dense(q_scales, "q_scales", dev, (T, n), torch.float32, where)
         else:
             sp = _dense(q_scales, "q_scales", dev, (T,), torch.float32, where)
-    _check(_lib.lora_rmsnorm(dev, xp, ldx, ptr[0], ld[0], ptr[1], ld[1], wp, eps, ptr[2], ld[2], ptr[3], ld[3], sp, group,
-                             T, d, _stream_on(stream, dev)), where)
+    _check(_lib.lora_rmsnorm(dev, xp, ldx, rp, ldr, op, ldo, wp, eps, yp, ldy, qp, ldq, sp, group, T, d,
+                             _stream_on(stream, dev)), where)
 
 
 def lora_get_error(pool: PoolHandle, stream=None) -> int:

@@ -1121,8 +1121,16 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(KvView kv, KvSeqs
 
 using AttendKernel = void (*)(KvView, KvSeqs, AttendArgs);
 
-// Steps of about 8 KiB: several tiles where a tile is small, so that the cost
-// of a step (a wait, the running maximum) is spread over as many bytes.
+// Which kernel takes a cache and a number of heads:
+//  - a step has as many tiles as give it about 8 KiB, so that its own cost (a
+//    wait, the running maximum) is spread over as many bytes: one tile instead of
+//    two took 127 instead of 119 us for 512 requests of e4m3, 32 / 8 heads of 128;
+//  - 12 warps where their registers suffice (up to 8 heads a unit, dims up to 128):
+//    64 requests of bf16, 32 heads of 128, 191 us, with 8 warps 196; 512 of e4m3 143
+//    and 163 us at the time; 8 where accumulators would spill: 64 / 4 heads of 128,
+//    e4m3, 100 us, with 12 warps 118;
+//  - the usual widths are constants, others take the loops of the next larger one
+//    with a test for each 16 dims.
 struct Variant {
   AttendKernel kernel[2];  // up to 8 query heads per key head, more
   int tt, warps[2];
@@ -1140,11 +1148,11 @@ Variant variant() {
 
 template <int TYPE>
 Variant variant_of(int dim) {
-  constexpr int W = TYPE == LORA_KV_BF16 ? 1 : 2, N = TYPE == LORA_KV_BF16 ? 8 : 12;
-  if (dim == 64) return variant<TYPE, 64, false, 2 * W, N>();
-  if (dim == 128) return variant<TYPE, 128, false, W, N>();
+  constexpr int W = TYPE == LORA_KV_BF16 ? 1 : 2;
+  if (dim == 64) return variant<TYPE, 64, false, 2 * W, 12>();
+  if (dim == 128) return variant<TYPE, 128, false, W, 12>();
   if (dim == 256) return variant<TYPE, 256, false, 1, 8>();
-  return dim < 128 ? variant<TYPE, 128, true, W, N>() : variant<TYPE, 256, true, 1, 8>();
+  return dim < 128 ? variant<TYPE, 128, true, W, 12>() : variant<TYPE, 256, true, 1, 8>();
 }
 
 }  // namespace lora
