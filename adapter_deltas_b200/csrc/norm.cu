@@ -31,10 +31,17 @@ struct NormArgs {
   float *scales;
   long long ldx, ldr, lds, ldy, ldq;  // bytes
   float eps;
-  int group;  // 0: one scale per row
+  int group, log2_vecs;  // columns of a scale (0: the row), and log2 of its vectors
   int T, d;
   int tpr;    // threads per row
 };
+
+// The larger of two, a NaN where either is one.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
 
 template <int VPT>
 __global__ void __launch_bounds__(kNormMaxThreads) rmsnorm_kernel(NormArgs a) {
@@ -44,6 +51,12 @@ __global__ void __launch_bounds__(kNormMaxThreads) rmsnorm_kernel(NormArgs a) {
   const long long row = (long long)blockIdx.x * (blockDim.x / a.tpr) + slot;
   const int nv = a.d / 8, nw = a.tpr / 32;  // nw: warps of a row (0 when rows share one)
   const bool live = row < a.T;
+  // a thread's place in each operand; its vectors are `hop` bytes apart (half that in q)
+  const int hop = a.tpr * 16;
+  const uint8_t *x = a.x + row * a.ldx + lane * 16, *res = a.res ? a.res + row * a.ldr + lane * 16 : nullptr;
+  const uint8_t *weight = a.weight + lane * 16;
+  uint8_t *sum = a.sum ? a.sum + row * a.lds + lane * 16 : nullptr, *y = a.y ? a.y + row * a.ldy + lane * 16 : nullptr;
+  uint8_t *qs = a.q + row * a.ldq + lane * 8;
   griddep_wait();
   griddep_launch_dependents();
   float h[VPT][8];
@@ -53,9 +66,9 @@ __global__ void __launch_bounds__(kNormMaxThreads) rmsnorm_kernel(NormArgs a) {
     const int v = lane + i * a.tpr;
     xs[i] = rs[i] = w[i] = make_uint4(0, 0, 0, 0);
     if (live && v < nv) {
-      w[i] = __ldg(reinterpret_cast<const uint4 *>(a.weight) + v);
-      xs[i] = *reinterpret_cast<const uint4 *>(a.x + row * a.ldx + v * 16);
-      if (a.res) rs[i] = *reinterpret_cast<const uint4 *>(a.res + row * a.ldr + v * 16);
+      w[i] = __ldg(reinterpret_cast<const uint4 *>(weight + i * hop));
+      xs[i] = *reinterpret_cast<const uint4 *>(x + i * hop);
+      if (res) rs[i] = *reinterpret_cast<const uint4 *>(res + i * hop);
     }
   }
   float ss = 0.f;
@@ -82,26 +95,29 @@ __global__ void __launch_bounds__(kNormMaxThreads) rmsnorm_kernel(NormArgs a) {
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
     const int v = lane + i * a.tpr;
-    if (live && v < nv && a.sum)
-      *reinterpret_cast<uint4 *>(a.sum + row * a.lds + v * 16) =
+    if (live && v < nv && sum)
+      *reinterpret_cast<uint4 *>(sum + i * hop) =
           make_uint4(pack_bf16x2(h[i][0], h[i][1]), pack_bf16x2(h[i][2], h[i][3]), pack_bf16x2(h[i][4], h[i][5]),
                      pack_bf16x2(h[i][6], h[i][7]));
     float g[8];
     unpack8(w[i], g);
 #pragma unroll
     for (int e = 0; e < 8; ++e) h[i][e] = h[i][e] * inv * g[e];
-    if (live && v < nv && a.y)
-      *reinterpret_cast<uint4 *>(a.y + row * a.ldy + v * 16) =
+    if (live && v < nv && y)
+      *reinterpret_cast<uint4 *>(y + i * hop) =
           make_uint4(pack_bf16x2(h[i][0], h[i][1]), pack_bf16x2(h[i][2], h[i][3]), pack_bf16x2(h[i][4], h[i][5]),
                      pack_bf16x2(h[i][6], h[i][7]));
   }
   if (!a.q) return;  // (the same for the whole grid)
+  float *scales = a.scales + row * (a.group ? nv >> a.log2_vecs : 1);
   uint32_t m[VPT];
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
-    m[i] = 0;
+    // (past the row x, residual and weight are 0, and so is h, unless the row's inv is not finite)
+    float top = fabsf(h[i][0]);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) m[i] = max(m[i], lane + i * a.tpr < nv ? abs_bits(h[i][e]) : 0u);
+    for (int e = 1; e < 8; ++e) top = max_nan(top, fabsf(h[i][e]));
+    m[i] = lane + i * a.tpr < nv ? __float_as_uint(top) & 0x7fffffffu : 0u;
   }
   if (a.group) {
     const int lanes = a.group / 8;
@@ -132,12 +148,12 @@ __global__ void __launch_bounds__(kNormMaxThreads) rmsnorm_kernel(NormArgs a) {
     const int v = lane + i * a.tpr;
     if (!live || v >= nv) continue;
     const Quant q = quant_of<448>(__uint_as_float(m[i]));
-    *reinterpret_cast<uint2 *>(a.q + row * a.ldq + v * 8) =
+    *reinterpret_cast<uint2 *>(qs + i * (hop / 2)) =
         make_uint2(code4<LORA_KV_E4M3>(h[i], q), code4<LORA_KV_E4M3>(h[i] + 4, q));
     if (a.group) {
-      if (v % (a.group / 8) == 0) a.scales[row * (a.d / a.group) + v / (a.group / 8)] = q.scale;
+      if ((v & ((1 << a.log2_vecs) - 1)) == 0) scales[v >> a.log2_vecs] = q.scale;
     } else if (v == 0) {
-      a.scales[row] = q.scale;
+      *scales = q.scale;
     }
   }
 }
@@ -226,6 +242,7 @@ int lora_rmsnorm(int device, const void *x, int ldx, const void *residual, int l
   a.ldq = ldq;
   a.eps = eps;
   a.group = group;
+  for (a.log2_vecs = 0; group > 8 << a.log2_vecs;) ++a.log2_vecs;
   a.T = T;
   a.d = d;
   const int nv = d / 8;
