@@ -33,8 +33,9 @@
  *    d_in, d_out, ldx and ldy must be multiples of 8, else LORA_ERR_ALIGNMENT.
  *  - x and y must not overlap.
  *  - Errors found on the device (bad adapter ids, timed-out waits) do not
- *    fault: the affected rows are left untouched and a sticky per-pool status
- *    word records the first error; read it with lora_get_error.
+ *    fault: the affected rows are left untouched and a sticky status word of the
+ *    pool (or key/value cache) records the first error; read it with
+ *    lora_get_error (lora_kv_get_error).
  */
 #ifndef LORA_B200_H
 #define LORA_B200_H
