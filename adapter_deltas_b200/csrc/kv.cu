@@ -73,11 +73,12 @@ __device__ __forceinline__ void locate_rows(const KvView &kv, const KvSeqs &s, i
   const int i = threadIdx.x;
   if (i < rows) {
     const int t = first + i;
-    int seq = t, back = 1, own = 1;  // the row's distance from its sequence's end; the sequence's rows
+    int seq = t, back = 1;  // the row's distance from its sequence's end
+    long long own = 1;      // the sequence's rows (of offsets in error more than 32 bits hold)
     if (s.offsets) {
       seq = tok[i];
       back = (int)tile[i] - t;
-      own = (int)tile[i] - (int)(tile[i] >> 32);
+      own = (long long)(int)tile[i] - (tile[i] >> 32);
     }
     long long at = -1;
     int row = 0;

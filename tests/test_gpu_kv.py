@@ -203,7 +203,9 @@ def test_bad_lengths_pages_and_offsets_are_reported_and_skipped(cuda_device):
             assert c.error() == L.LORA_OK and torch.equal(before, c.mem)
         # offsets out of order or past the rows
         _, k, v = b.rows()
-        for off in ([0, 30, 20, 60, 80], [0, 20, 40, 60, 81], [-1, 20, 40, 60, 80]):
+        lowest, highest = -(1 << 31), (1 << 31) - 1
+        for off in ([0, 30, 20, 60, 80], [0, 20, 40, 60, 81], [-1, 20, 40, 60, 80], [lowest, highest, highest, highest, highest],
+                    [lowest, lowest, -1, highest, highest], [highest, 20, 40, 60, lowest]):
             L.lora_kv_append(c.kv, 0, k.to(cuda_device), v.to(cuda_device), c.table, c.lens,
                              torch.tensor(off, dtype=torch.int32, device=cuda_device))
             assert c.error() == L.LORA_ERR_BAD_ID
