@@ -53,6 +53,7 @@ constexpr int kAttMaxStages = 8;
 constexpr int kAttSmem = 227 * 1024;
 constexpr int kSlack = 4, kVSlack = 2;  // powers of two
 constexpr int kCutSteps = 3;
+constexpr int kMaxSlotsLog2 = 30;  // of a block: counted in 32 bits
 
 struct AttendArgs {
   const uint8_t *q;
@@ -355,6 +356,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(KvView kv, KvSeqs
   };
 
   const unsigned long long slots_all = (unsigned long long)(total & kSlotBits) * a.units;
+  const bool too_long = slots_all > (unsigned long long)gridDim.x << kMaxSlotsLog2;
   const unsigned long long units_all = (unsigned long long)(total >> kCountAt) * a.units;
   // A unit cut between blocks costs their last one a few steps' time, in each
   // warp.  While blocks of whole units are not longer than that, none is cut.
@@ -366,7 +368,8 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(KvView kv, KvSeqs
   const unsigned long long each = quotient(items, max(blocks, 1u));  // items of a block; the first `more` have one more
   const unsigned more = (unsigned)(items - each * blocks);
   long long b0 = each * blockIdx.x + min(blockIdx.x, more);
-  int slots = blockIdx.x < blocks ? (int)each + (blockIdx.x < more) : 0;
+  int slots = blockIdx.x < blocks && !too_long ? (int)each + (blockIdx.x < more) : 0;
+  if (too_long && tid == 0) set_status(kv.status, LORA_ERR_BAD_ID);
   if (by_units) {  // from units to slots: warp 0 the first unit's start, warp 1 the last one's end
     if (slots > 0 && warp < 2) {
       const long long u = warp ? b0 + slots - 1 : b0, y = quotient(u, a.units);

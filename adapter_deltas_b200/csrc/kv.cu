@@ -492,7 +492,7 @@ int lora_kv_gather(lora_kv *kv, int layer, void *k, int ldk, void *v, int ldv, c
 }
 
 size_t lora_attend_workspace_bytes(const lora_kv *kv, int n_heads) {
-  if (!kv || n_heads < kv->heads || n_heads % kv->heads) return 0;
+  if (!kv || n_heads < kv->heads || n_heads % kv->heads || n_heads > kKvMaxQHeads) return 0;
   return attend_workspace_bytes(kv, n_heads);
 }
 

@@ -117,10 +117,6 @@ __device__ __forceinline__ float quant_div(float x, const Quant &q) {
   return fmaf(fmaf(-t, q.amax, a), q.rcp, t);
 }
 
-// |x| as bits order like the magnitudes, with every NaN above infinity: the
-// maximum over bits does not lose a NaN as fmaxf would.
-__device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
-
 // Two fp32 values as two e4m3 bytes (nearest even, values past 448 as 448, NaN kept).
 __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
   uint16_t r;

@@ -55,7 +55,7 @@ CASES = [  # heads, kv_heads, dim, page, lens
     (10, 5, 80, 16, [40, 111]),
     (12, 4, 96, 128, [130, 260]),
     (24, 2, 256, 16, [18, 100]),
-    (16, 1, 192, 1024, [1030]),
+    (16, 1, 208, 1024, [1030]),
     (9, 1, 48, 32, [70] * 20),
     (40, 2, 32, 16, [200, 33]),
     (64, 1, 128, 16, [500, 3]),
@@ -206,13 +206,33 @@ def test_bad_lengths_and_pages(cuda_device):
             assert ((out[1].view(-1, 64).double() - o).abs() <= tol).all()
 
 
+def test_a_batch_past_the_counters_is_reported(cuda_device):
+    """64 sequences of 2^30 tokens that share one page, 1024 heads: past 2^30 steps an SM; nothing is attended to."""
+    b = R.Batch([1, 0], 1024, 16, 1024, seed=15)
+    with Cache(b, "bf16", cuda_device) as c:
+        c.append()
+        assert c.error() == L.LORA_OK
+        lens = torch.full((66,), 1 << 30, dtype=torch.int32, device=cuda_device)
+        lens[5], lens[6] = 0, -1
+        table = torch.zeros(66, 1 << 20, dtype=torch.int32, device=cuda_device)
+        q = torch.zeros(66, 1024 * 16, dtype=torch.bfloat16, device=cuda_device)
+        out = torch.full_like(q, 7.0)
+        ws = torch.empty(L.lora_attend_workspace_bytes(c.kv, 1024), dtype=torch.uint8, device=cuda_device)
+        L.lora_attend(c.kv, 0, q, out, table, lens, ws)
+        assert c.error() == L.LORA_ERR_BAD_ID
+        keep = torch.arange(66) != 5
+        assert (out[5] == 0).all() and (out.cpu()[keep] == 7.0).all()
+        few = queries(b, 1024, 15)
+        check(c, "bf16", few, *attend(c, few, ws=ws))
+
+
 def test_refusals(cuda_device):
     b = R.Batch([20, 20], 2, 64, 16, seed=10)
     q = queries(b, 4, 10).to(cuda_device)
     with Cache(b, "bf16", cuda_device) as c:
         out, lse = torch.empty_like(q), torch.empty(2, 4, device=cuda_device)
         ws = torch.empty(L.lora_attend_workspace_bytes(c.kv, 4), dtype=torch.uint8, device=cuda_device)
-        assert L.lora_attend_workspace_bytes(c.kv, 3) == 0 and L.lora_attend_workspace_bytes(c.kv, 0) == 0
+        assert all(L.lora_attend_workspace_bytes(c.kv, n) == 0 for n in (3, 0, -2, 4098))
 
         def code(layer=0, q=q, out=out, table=c.table, lens=c.lens, ws=ws, **more):
             with pytest.raises((L.LoraError, ValueError)) as e:
