@@ -358,9 +358,13 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(KvView kv, KvSeqs
   const unsigned long long slots_all = (unsigned long long)(total & kSlotBits) * a.units;
   const bool too_long = slots_all > (unsigned long long)gridDim.x << kMaxSlotsLog2;
   const unsigned long long units_all = (unsigned long long)(total >> kCountAt) * a.units;
-  // A unit cut between blocks costs their last one a few steps' time, in each
-  // warp.  While blocks of whole units are not longer than that, none is cut.
-  const bool by_units = (units_all + gridDim.x - 1) * longest <= slots_all + (unsigned long long)kCutSteps * n_warps * gridDim.x;
+  // A unit cut between blocks costs their last one about 3 steps' time, in each
+  // warp.  While blocks of whole units are longer by less than that, none is cut
+  // (attention alone, whole and cut: 16 requests of up to 100 tokens 10.1 and 15.3
+  // us, 256 requests with a window of 128 20.1 and 23.2; 64 requests of 200 to 4000
+  // tokens 319 and 187, which are cut).
+  const unsigned long long most_units = quotient(units_all + gridDim.x - 1, gridDim.x);  // of a block
+  const bool by_units = most_units * longest * gridDim.x <= slots_all + (unsigned long long)kCutSteps * n_warps * gridDim.x;
   // (two slots at least to a block, so that it has a step: the join counts on
   // every block in a row having a part)
   const unsigned long long items = by_units ? units_all : slots_all;
