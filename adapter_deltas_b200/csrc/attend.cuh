@@ -217,18 +217,63 @@ __device__ __forceinline__ Ends finish(const float *sinks, int head, float m, fl
   return e;
 }
 
-// y += w * 8 values of a state (FAR: written by another block, read past L1).
-template <bool FAR = false>
-__device__ __forceinline__ void add8(float (&y)[8], float w, const float4 *p) {
+// 8 dims of a row's joined states.  add() takes states first, first + step, .. below
+// end, N at a time: their loads do not wait for one another, so that a join
+// takes one trip to memory per N states (maxima first and sums then took 5 us for
+// two states of 16 x 256; FAR: written by another block, read past L1).
+struct Joined {
+  float m = -INFINITY, l = 0.f, y[8] = {};
+  bool gone = false;  // a block that gave up is among them
+
+  template <int N, bool FAR, class At>
+  __device__ __forceinline__ void add(int first, int end, int step, At at, int row, int rows, int sums) {
+    auto ld = [](const float *p) { return FAR ? __ldcg(p) : *p; };
+    auto ld4 = [](const float *p) {
+      return FAR ? __ldcg(reinterpret_cast<const float4 *>(p)) : *reinterpret_cast<const float4 *>(p);
+    };
+#pragma unroll 1
+    for (int i = first; i < end; i += N * step) {
+      float ms[N], ls[N];
+      float4 z[N][2];
 #pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    const float4 z = FAR ? __ldcg(p + k) : p[k];
-    y[4 * k] = fmaf(w, z.x, y[4 * k]);
-    y[4 * k + 1] = fmaf(w, z.y, y[4 * k + 1]);
-    y[4 * k + 2] = fmaf(w, z.z, y[4 * k + 2]);
-    y[4 * k + 3] = fmaf(w, z.w, y[4 * k + 3]);
+      for (int k = 0; k < N; ++k) {
+        ms[k] = -INFINITY;
+        ls[k] = 0.f;
+        z[k][0] = z[k][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (i + k * step < end) {
+          const float *st = at(i + k * step);
+          ms[k] = ld(st + row);
+          ls[k] = ld(st + rows + row);
+          z[k][0] = ld4(st + sums);
+          z[k][1] = ld4(st + sums + 4);
+        }
+      }
+      float top = m;
+#pragma unroll
+      for (int k = 0; k < N; ++k) {
+        top = fmaxf(top, ms[k]);
+        gone |= ls[k] < 0.f;
+      }
+      const float base = top == -INFINITY ? 0.f : top, fade = exp2_fast(m - base);
+      m = top;
+      l *= fade;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) y[e] *= fade;
+#pragma unroll
+      for (int k = 0; k < N; ++k) {
+        const float w = exp2_fast(ms[k] - base);
+        l = fmaf(w, ls[k], l);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          y[4 * h] = fmaf(w, z[k][h].x, y[4 * h]);
+          y[4 * h + 1] = fmaf(w, z[k][h].y, y[4 * h + 1]);
+          y[4 * h + 2] = fmaf(w, z[k][h].z, y[4 * h + 2]);
+          y[4 * h + 3] = fmaf(w, z[k][h].w, y[4 * h + 3]);
+        }
+      }
+    }
   }
-}
+};
 __device__ __forceinline__ void store8(uint8_t *out, const float (&y)[8], float mul) {
   *reinterpret_cast<uint4 *>(out) =
       make_uint4(pack_bf16x2(y[0] * mul, y[1] * mul), pack_bf16x2(y[2] * mul, y[3] * mul),
@@ -963,6 +1008,31 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(KvView kv, KvSeqs
       run[__popc(firsts)] = __popc(there);
     }
   }
+  // Meanwhile a thread each for the unit this block begins in (warp 1) and the
+  // one it ends in (2): whether the block's border cuts it, into which blocks, and
+  // a first look at their counter.
+  int cut_first = 0, cut_count = 0;
+  unsigned long long cut_seen = 0;
+  if ((warp == 1 || warp == 2) && lane == 0) {
+    const int which = warp - 1;
+    to_join[which] = make_int2(0, 0);
+    if (slots > 0) {
+      const int at = which ? n_warps : 0;
+      const int n = unit_slots(start[at].y, a.window, TT);
+      const int in = (int)(from[at] - quotient(from[at], n) * n);  // slot of its unit
+      // the unit's first and last step's slots in the list
+      const long long here = which ? b0 + slots - 1 : b0, s_first = here - in + 1, s_last = here - in + n - 1;
+      if (which ? in > 0 && s_last > here && s_first >= b0 : in > 1) {
+        auto block_of = [&](unsigned long long slot) {
+          const unsigned long long big = (each + 1) * more;
+          return (int)(slot < big ? quotient(slot, each + 1) : more + quotient(slot - big, each));
+        };
+        cut_first = block_of(s_first);
+        cut_count = block_of(s_last) - cut_first + 1;
+        cut_seen = __ldcg(a.done + cut_first);
+      }
+    }
+  }
   __syncthreads();
   // a thread has 8 dims of a row
   const int octs = dim / 8;
@@ -975,128 +1045,105 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(KvView kv, KvSeqs
     const bool whole = !(p0.z & 1) && !(p1.z & 2);
     const int kvh = unit_kvh(p0.y), h0 = unit_h0(p0.y);
     if (h0 + r >= a.group) continue;
-    float mm = -INFINITY, ll = 0.f;
-#pragma unroll 1
-    for (int i = f; i < e; ++i) mm = fmaxf(mm, where[order[i]][r]);
-    const float bm = mm == -INFINITY ? 0.f : mm;
-    float y[8] = {};
-#pragma unroll 2
-    for (int i = f; i < e; ++i) {
-      const float *st = where[order[i]];
-      const float w = exp2_fast(st[r] - bm);
-      ll = fmaf(w, st[a.rows + r], ll);
-      add8(y, w, reinterpret_cast<const float4 *>(st + state_head(a.rows) + r * dim + d));
-    }
+    Joined x;
+    x.add<4, false>(f, e, 1, [&](int i) { return where[order[i]]; }, r, a.rows, state_head(a.rows) + r * dim + d);
     if (whole) {
       const int hd = kvh * a.group + h0 + r;
-      const Ends fin = finish(a.sinks, hd, mm, ll);
+      const Ends fin = finish(a.sinks, hd, x.m, x.l);
       if (a.lse && d == 0) a.lse[(long long)p0.x * a.n_heads + hd] = fin.lse;
-      store8(a.out + p0.x * a.ldo + ((long long)hd * dim + d) * 2, y, fin.mul);
+      store8(a.out + p0.x * a.ldo + ((long long)hd * dim + d) * 2, x.y, fin.mul);
     } else {
       float *st = a.part + ((size_t)blockIdx.x * 2 + (p0.z & 1 ? 0 : 1)) * floats;
       if (d == 0) {
-        st[r] = mm;
-        st[a.rows + r] = ll;
+        st[r] = x.m;
+        st[a.rows + r] = x.l;
       }
       float4 *to = reinterpret_cast<float4 *>(st + state_head(a.rows) + r * dim + d);
-      to[0] = make_float4(y[0], y[1], y[2], y[3]);
-      to[1] = make_float4(y[4], y[5], y[6], y[7]);
+      to[0] = make_float4(x.y[0], x.y[1], x.y[2], x.y[3]);
+      to[1] = make_float4(x.y[4], x.y[5], x.y[6], x.y[7]);
     }
   }
   __syncthreads();
 
-  // ---- count this block in for the units its borders cut (thread 0: the one it
-  // begins in, thread 32: the one it ends in); the last of a unit's blocks joins
-  if (tid == 0 || tid == 32) {
-    const int which = tid >> 5;
-    to_join[which] = make_int2(0, 0);
-    if (slots > 0) {
-      const int at = which ? n_warps : 0;
-      const int n = unit_slots(start[at].y, a.window, TT);
-      const int in = (int)(from[at] - quotient(from[at], n) * n);  // slot of its unit
-      // the unit's first and last step's slots in the list
-      const long long here = which ? b0 + slots - 1 : b0, s_first = here - in + 1, s_last = here - in + n - 1;
-      const bool cut = which ? in > 0 && s_last > here && s_first >= b0 : in > 1;
-      if (cut) {
-        auto block_of = [&](unsigned long long slot) {
-          const unsigned long long big = (each + 1) * more;
-          return (int)(slot < big ? quotient(slot, each + 1) : more + quotient(slot - big, each));
-        };
-        const int b_first = block_of(s_first), b_last = block_of(s_last);
-        if (broken)  // (no result for what this block was to add to)
+  // ---- count this block in for the units its borders cut; the last of a unit's blocks joins
+  if (cut_count) {
+    if (broken)  // (no result for what this block was to add to)
 #pragma unroll 1
-          for (int r = 0; r < a.rows; ++r) a.part[((size_t)blockIdx.x * 2 + which) * floats + a.rows + r] = -1.f;
-        __threadfence();
-        unsigned long long seen = atomicAdd(a.done + b_first, 0ull), next;
-        do {
-          next = (seen >> kCountBits) == a.tag ? seen + 1 : a.tag << kCountBits | 1;
-          const unsigned long long was = atomicCAS(a.done + b_first, seen, next);
-          if (was == seen) break;
-          seen = was;
-        } while (true);
-        __threadfence();
-        if ((int)(next & ((1u << kCountBits) - 1u)) == b_last - b_first + 1) {
-          a.done[b_first] = 0;
-          to_join[which] = make_int2(b_first, b_last - b_first + 1);
-        }
-      }
+      for (int r = 0; r < a.rows; ++r) a.part[((size_t)blockIdx.x * 2 + warp - 1) * floats + a.rows + r] = -1.f;
+    __threadfence();
+    unsigned long long next;
+    do {
+      next = (cut_seen >> kCountBits) == a.tag ? cut_seen + 1 : a.tag << kCountBits | 1;
+      const unsigned long long was = atomicCAS(a.done + cut_first, cut_seen, next);
+      if (was == cut_seen) break;
+      cut_seen = was;
+    } while (true);
+    __threadfence();
+    if ((int)(next & ((1u << kCountBits) - 1u)) == cut_count) {
+      a.done[cut_first] = 0;
+      to_join[warp - 1] = make_int2(cut_first, cut_count);
     }
   }
   __syncthreads();
+  if (to_join[0].y + to_join[1].y) {
+    // Both units' rows by all threads, 8 dims of a row each; where they are fewer
+    // than the threads the parts are shared out among groups of them.
+    int seq[2], kvh[2], h0[2], items[2];
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+      const int at = which ? n_warps : 0;
+      items[which] = 0;
+      if (!to_join[which].y) continue;
+      const int un = (int)quotient(from[at], unit_slots(start[at].y, a.window, TT));
+      seq[which] = start[at].x;
+      kvh[which] = un / a.head_groups;
+      h0[which] = (un - kvh[which] * a.head_groups) * ROWS;
+      items[which] = min(a.rows, a.group - h0[which]) * octs;
+    }
+    const int all = items[0] + items[1];
+    const int groups = max(1, min((int)blockDim.x / all, max(to_join[0].y, to_join[1].y)));
+    Joined *share = reinterpret_cast<Joined *>(smem);  // (the rings are idle)
+    auto put = [&](const Joined &x, int which, int r, int d) {
+      if (x.gone) return;  // (the row stays as it was)
+      const int hd = (which ? kvh[1] : kvh[0]) * a.group + (which ? h0[1] : h0[0]) + r;
+      const long long row = which ? seq[1] : seq[0];
+      const Ends e = finish(a.sinks, hd, x.m, x.l);
+      if (a.lse && d == 0) a.lse[row * a.n_heads + hd] = e.lse;
+      store8(a.out + row * a.ldo + ((long long)hd * dim + d) * 2, x.y, e.mul);
+    };
 #pragma unroll 1
-  for (int which = 0; which < 2; ++which) {
-    const int2 job = to_join[which];
-    if (!job.y) continue;
-    const int unit = which ? n_warps : 0, seq = start[unit].x;
-    const int un = (int)quotient(from[unit], unit_slots(start[unit].y, a.window, TT));
-    const int kvh = un / a.head_groups, h0 = (un - kvh * a.head_groups) * ROWS, live = min(a.rows, a.group - h0);
-    // the first block's own part (1), then those after it (0)
-    auto state = [&](int i) { return a.part + ((size_t)(job.x + i) * 2 + (i ? 0 : 1)) * floats; };
-    float *weight = reinterpret_cast<float *>(smem);  // [parts][rows], behind it [rows] maxima and sums (the rings are idle)
-    float *tops = weight + job.y * a.rows, *totals = tops + a.rows;
+    for (int i = tid; i < all * groups; i += blockDim.x) {
+      const int grp = i / all, which = i - grp * all >= items[0], at = i - grp * all - (which ? items[0] : 0);
+      const int r = at / octs, d = (at - r * octs) * 8;
+      const int2 job = to_join[which];
+      // the first block's own part (1), then those after it (0)
+      auto state = [&](int k) { return a.part + ((size_t)(job.x + k) * 2 + (k ? 0 : 1)) * floats; };
+      Joined x;
+      x.add<8, true>(grp, job.y, groups, state, r, a.rows, state_head(a.rows) + r * dim + d);
+      if (groups == 1)
+        put(x, which, r, d);
+      else
+        share[i] = x;
+    }
+    if (groups > 1) {
+      __syncthreads();
+      if (tid < all) {
+        const int which = tid >= items[0], at = tid - (which ? items[0] : 0), r = at / octs;
+        Joined x;
 #pragma unroll 1
-    for (int r = warp; r < live; r += n_warps) {
-      float mm = -INFINITY, ll = 0.f;
-      bool none = false;
-#pragma unroll 1
-      for (int i = lane; i < job.y; i += 32) {
-        mm = fmaxf(mm, __ldcg(state(i) + r));
-        none |= __ldcg(state(i) + a.rows + r) < 0.f;
-      }
-      for (int d = 16; d; d >>= 1) mm = fmaxf(mm, __shfl_xor_sync(~0u, mm, d));
-      const float bm = mm == -INFINITY ? 0.f : mm;
-#pragma unroll 1
-      for (int i = lane; i < job.y; i += 32) {
-        const float w = exp2_fast(__ldcg(state(i) + r) - bm);
-        weight[i * a.rows + r] = w;
-        ll = fmaf(w, __ldcg(state(i) + a.rows + r), ll);
-      }
-      for (int d = 16; d; d >>= 1) ll += __shfl_xor_sync(~0u, ll, d);
-      if (__any_sync(~0u, none)) ll = -1.f;
-      if (lane == 0) {
-        tops[r] = mm;
-        totals[r] = ll;
+        for (int k = 0; k < groups; ++k) {  // (a group without a part has the empty state)
+          const Joined &z = share[k * all + tid];
+          const float top = fmaxf(x.m, z.m), base = top == -INFINITY ? 0.f : top;
+          const float u = exp2_fast(x.m - base), w = exp2_fast(z.m - base);
+          x.m = top;
+          x.l = fmaf(w, z.l, x.l * u);
+          x.gone |= z.gone;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x.y[e] = fmaf(w, z.y[e], x.y[e] * u);
+        }
+        put(x, which, r, (at - r * octs) * 8);
       }
     }
-    __syncthreads();
-#pragma unroll 1
-    for (int x = tid; x < live * octs; x += blockDim.x) {
-      const int r = x / octs, d = (x - r * octs) * 8;
-      const float ll = totals[r];
-      if (ll < 0.f) continue;  // (a block that gave up: the row stays as it was)
-      float y[8] = {};
-      const size_t at = state_head(a.rows) + r * dim + d;
-      add8<true>(y, weight[r], reinterpret_cast<const float4 *>(state(0) + at));
-      const float *rest = state(1) + at;
-#pragma unroll 4
-      for (int i = 1; i < job.y; ++i)
-        add8<true>(y, weight[i * a.rows + r], reinterpret_cast<const float4 *>(rest + (size_t)(i - 1) * 2 * floats));
-      const int hd = kvh * a.group + h0 + r;
-      const Ends e = finish(a.sinks, hd, tops[r], ll);
-      if (a.lse && d == 0) a.lse[(long long)seq * a.n_heads + hd] = e.lse;
-      store8(a.out + seq * a.ldo + ((long long)hd * dim + d) * 2, y, e.mul);
-    }
-    __syncthreads();
   }
 
   // ---- sequences without a token: zeros, or untouched (length -1, and lengths in error)
