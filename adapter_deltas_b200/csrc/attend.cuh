@@ -1046,7 +1046,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(KvView kv, KvSeqs
     const int kvh = unit_kvh(p0.y), h0 = unit_h0(p0.y);
     if (h0 + r >= a.group) continue;
     Joined x;
-    x.add<4, false>(f, e, 1, [&](int i) { return where[order[i]]; }, r, a.rows, state_head(a.rows) + r * dim + d);
+    x.add<2, false>(f, e, 1, [&](int i) { return where[order[i]]; }, r, a.rows, state_head(a.rows) + r * dim + d);
     if (whole) {
       const int hd = kvh * a.group + h0 + r;
       const Ends fin = finish(a.sinks, hd, x.m, x.l);
@@ -1119,7 +1119,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(KvView kv, KvSeqs
       // the first block's own part (1), then those after it (0)
       auto state = [&](int k) { return a.part + ((size_t)(job.x + k) * 2 + (k ? 0 : 1)) * floats; };
       Joined x;
-      x.add<8, true>(grp, job.y, groups, state, r, a.rows, state_head(a.rows) + r * dim + d);
+      x.add<4, true>(grp, job.y, groups, state, r, a.rows, state_head(a.rows) + r * dim + d);
       if (groups == 1)
         put(x, which, r, d);
       else
