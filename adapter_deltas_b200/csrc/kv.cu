@@ -13,8 +13,10 @@
 // shuffles.  A block takes `rows` consecutive rows of the batch, so
 // many that the blocks are resident at once (its start, a chain of dependent
 // reads, is then paid once); a thread's loads of 64 bytes are in flight
-// together.  What bounds the 8-bit forms beside HBM is the instructions per
-// element, so addresses are kept per thread and stepped.  The block's warps look up the rows' sequences (a 32-way search in
+// together.  What bounds the 8-bit append beside HBM is the instructions per
+// element, so addresses are kept per thread and stepped.  4096 rows of 32 heads of
+// 128 as e4m3: append 25 us (102 MB, 4.1 TB/s), gather of 11734 rows 62 us (291 MB,
+// two thirds of them written, 4.7 TB/s); 512 rows of 8 heads 4 us.  The block's warps look up the rows' sequences (a 32-way search in
 // row_offsets, two dependent reads up to 1024 sequences, where the row before is
 // not in the same one), then a thread a row its length and page; append reads
 // its first input rows, which do not depend on that, before.
@@ -217,8 +219,8 @@ __global__ void __launch_bounds__(kRowThreads, kRowBlocks) kv_append_kernel(KvVi
       for (int k = 0; k < U; ++k) {
         float x[8];
         unpack8(u[i][k], x);
-        c[2 * k] = code4<TYPE>(x, q);
-        c[2 * k + 1] = code4<TYPE>(x + 4, q);
+        c[2 * k] = code4<TYPE, true>(x, q);
+        c[2 * k + 1] = code4<TYPE, true>(x + 4, q);
       }
       if (on) *held(kv.base + at, tok[row], which, head) = make_uint4(c[0], c[1], c[2 * U - 2], c[2 * U - 1]);
       if (part == 0) *held.scale(kv.base + at, tok[row], which, head) = q.scale;

@@ -111,10 +111,35 @@ __device__ __forceinline__ Quant quant_of(float amax) {
   if (none) q.rcp = 0.f;
   return q;
 }
-// x * qmax / amax.
+// x * qmax / amax, and the same for two values with the packed fp32 instructions,
+// half as many (append of 4096 rows, 32 heads of 128: 25.1 and 27.3 us; the
+// norm has no registers left for the pairs: 48.3 and 49.4 us for 8192 x 4096).
 __device__ __forceinline__ float quant_div(float x, const Quant &q) {
   const float a = x * q.mul, t = a * q.rcp;
   return fmaf(fmaf(-t, q.amax, a), q.rcp, t);
+}
+__device__ __forceinline__ unsigned long long pair2(float lo, float hi) {
+  unsigned long long r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ unsigned long long mul2(unsigned long long a, unsigned long long b) {
+  unsigned long long r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ unsigned long long fma2(unsigned long long a, unsigned long long b, unsigned long long c) {
+  unsigned long long r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ float2 quant_div(float x, float y, const Quant &q) {
+  const unsigned long long rcp = pair2(q.rcp, q.rcp);
+  const unsigned long long a = mul2(pair2(x, y), pair2(q.mul, q.mul)), t = mul2(a, rcp);
+  const unsigned long long z = fma2(fma2(t, pair2(-q.amax, -q.amax), a), rcp, t);
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(z));
+  return r;
 }
 
 // Two fp32 values as two e4m3 bytes (nearest even, values past 448 as 448, NaN kept).
@@ -129,11 +154,18 @@ __device__ __forceinline__ uint32_t int8x4(float a, float b, float c, float d) {
   const int k = min(127, max(-127, __float2int_rn(c))), l = min(127, max(-127, __float2int_rn(d)));
   return (i & 255) | (j & 255) << 8 | (k & 255) << 16 | (uint32_t)(l & 255) << 24;
 }
-template <int TYPE>
+template <int TYPE, bool PAIRS>
 __device__ __forceinline__ uint32_t code4(const float *x, const Quant &q) {
-  const float a = quant_div(x[0], q), b = quant_div(x[1], q), c = quant_div(x[2], q), d = quant_div(x[3], q);
-  if (TYPE == LORA_KV_E4M3) return e4m3x2(a, b) | e4m3x2(c, d) << 16;
-  return int8x4(a, b, c, d);
+  float2 lo, hi;
+  if (PAIRS) {
+    lo = quant_div(x[0], x[1], q);
+    hi = quant_div(x[2], x[3], q);
+  } else {
+    lo = make_float2(quant_div(x[0], q), quant_div(x[1], q));
+    hi = make_float2(quant_div(x[2], q), quant_div(x[3], q));
+  }
+  if (TYPE == LORA_KV_E4M3) return e4m3x2(lo.x, lo.y) | e4m3x2(hi.x, hi.y) << 16;
+  return int8x4(lo.x, lo.y, hi.x, hi.y);
 }
 
 // Four held bytes as the numbers they encode (before the scale).

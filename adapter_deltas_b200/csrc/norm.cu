@@ -149,7 +149,7 @@ __global__ void __launch_bounds__(kNormMaxThreads) rmsnorm_kernel(NormArgs a) {
     if (!live || v >= nv) continue;
     const Quant q = quant_of<448>(__uint_as_float(m[i]));
     *reinterpret_cast<uint2 *>(qs + i * (hop / 2)) =
-        make_uint2(code4<LORA_KV_E4M3>(h[i], q), code4<LORA_KV_E4M3>(h[i] + 4, q));
+        make_uint2(code4<LORA_KV_E4M3, false>(h[i], q), code4<LORA_KV_E4M3, false>(h[i] + 4, q));
     if (a.group) {
       if ((v & ((1 << a.log2_vecs) - 1)) == 0) scales[v >> a.log2_vecs] = q.scale;
     } else if (v == 0) {
