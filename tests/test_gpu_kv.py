@@ -160,6 +160,24 @@ def test_rows_as_slices_of_a_fused_projection(cuda_device):
         assert (both[:, 128:136] == 7.0).all()
 
 
+@pytest.mark.parametrize("kv_type", list(R.TYPES))
+@pytest.mark.parametrize("at,ld", [(0, 480), (8, 480), (16, 488), (24, 472), (16, 480)])
+def test_rows_at_16_and_32_bytes(cuda_device, kv_type, at, ld):
+    """Rows need start at multiples of 16 bytes only; where all start at 32 they are read and written 32 at a time."""
+    b = R.Batch([33, 1, 70], 2, 80, 16, seed=16)
+    off, k, v = b.rows()
+    wide = torch.zeros(len(k), ld, dtype=torch.bfloat16)
+    wide[:, at:at + 160], wide[:, at + 160:at + 320] = k, v
+    src, dst = wide.to(cuda_device), torch.full(wide.shape, 7.0, dtype=torch.bfloat16, device=cuda_device)
+    with Cache(b, kv_type, cuda_device) as c:
+        cut = lambda t: (t[:, at:at + 160], t[:, at + 160:at + 320])  # noqa: E731
+        L.lora_kv_append(c.kv, 0, *cut(src), c.table, c.lens, off.to(cuda_device))
+        L.lora_kv_gather(c.kv, 0, *cut(dst), c.table, c.lens, off.to(cuda_device))
+        assert same([x.cpu() for x in cut(dst)], c.expect(kv_type)) and c.error() == L.LORA_OK
+        dst[:, at:at + 320] = 7.0
+        assert (dst == 7.0).all()
+
+
 def test_layers_and_far_pages(cuda_device):
     """Layers are apart, and pages beyond 4 GiB of the cache are reached."""
     b = R.Batch([40, 17], 8, 128, 16, seed=7)
