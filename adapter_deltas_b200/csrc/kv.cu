@@ -10,13 +10,16 @@
 // Work split: a row of one head's K or V (a vector) is handled by `lanes`
 // neighbouring threads (a power of two), each with 16 bytes of the held row: 8
 // elements of bf16 or 16 in 8 bits, whose largest magnitude they reduce with
-// shuffles.  A block takes `rows` consecutive rows of the batch, so
-// many that the blocks are resident at once (its start, a chain of dependent
-// reads, is then paid once); a thread's loads of 64 bytes are in flight
-// together.  What bounds the 8-bit append beside HBM is the instructions per
-// element, so addresses are kept per thread and stepped.  4096 rows of 32 heads of
-// 128 as e4m3: append 25 us (102 MB, 4.1 TB/s), gather of 11734 rows 62 us (291 MB,
-// two thirds of them written, 4.7 TB/s); 512 rows of 8 heads 4 us.  The block's warps look up the rows' sequences (a 32-way search in
+// shuffles.  An append's block takes `rows` consecutive rows of the batch, so
+// many that the blocks are resident at once: its start, a chain of dependent
+// reads, is paid once, beside its first loads (4096 rows of 32 heads of 128 as
+// e4m3: 25 us, 102 MB at 4.1 TB/s; with 1 row a block 29).  What bounds the 8-bit
+// append beside HBM is the instructions per element, so addresses are kept per
+// thread and stepped.  A gather's block takes what its threads hold in flight
+// twice over: its accesses, 128 bytes of a head here and there, are then close in
+// time to the rest of their tiles (11734 rows of that cache: 50 us, 291 MB at
+// 5.8 TB/s; resident blocks of 16 rows 60, 1 row, which leaves threads idle, 63).
+// The block's warps look up the rows' sequences (a 32-way search in
 // row_offsets, two dependent reads up to 1024 sequences, where the row before is
 // not in the same one), then a thread a row its length and page; append reads
 // its first input rows, which do not depend on that, before.
@@ -28,6 +31,8 @@ namespace lora {
 
 constexpr int kRowThreads = 256, kRowBlocks = 5;  // blocks resident on an SM
 constexpr int kMaxBlockRows = 64;
+constexpr int kGatherAhead = 4;  // vectors of a thread in flight
+constexpr int kGatherTurns = 2;
 
 // Sequence of row t (largest s with off[s] <= t, if t < off[s + 1]), by one warp; -1 if none.
 __device__ __forceinline__ int find_seq(const int32_t *off, int n, int t) {
@@ -121,7 +126,7 @@ __host__ __device__ constexpr int vec_elements(int type) { return 16 / kv_elt(ty
 
 // A thread's 16 values of a bf16 row are 32 bytes.  As one access they are a sector
 // of its own; in two halves every sector is touched twice (gather of 11734 rows of
-// 32 heads of 128, e4m3: @ and 62 us).
+// 32 heads of 128, e4m3: 60 and 62 us before its blocks were cut to two turns).
 __device__ __forceinline__ void load32(const uint8_t *p, bool wide, uint4 &a, uint4 &b) {
   if (wide) {
     asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
@@ -257,7 +262,7 @@ __global__ void __launch_bounds__(kRowThreads, kRowBlocks) kv_append_kernel(KvVi
 
 template <int TYPE>
 __global__ void __launch_bounds__(kRowThreads, kRowBlocks) kv_gather_kernel(KvView kv, KvSeqs s, RowArgs a) {
-  constexpr int E = vec_elements(TYPE), kAhead = 4;
+  constexpr int E = vec_elements(TYPE), kAhead = kGatherAhead;
   __shared__ long long tile[kMaxBlockRows];
   __shared__ int tok[kMaxBlockRows];
   const int first = blockIdx.x * a.rows, rows = min(a.rows, a.T - first);
@@ -344,13 +349,18 @@ int check_row_call(const lora_kv *kv, int layer, const void *k, int ldk, const v
   return LORA_OK;
 }
 
+// turns: at most so many rows to a block as its threads take in so many turns (0: no such limit).
 template <class K>
-int launch_rows(K kernel, const lora_kv *kv, int layer, const KvSeqs &s, RowArgs a, cudaStream_t st) {
+int launch_rows(K kernel, const lora_kv *kv, int layer, const KvSeqs &s, RowArgs a, int turns, cudaStream_t st) {
   a.lanes = 1;
   while (a.lanes * vec_elements(kv->type) < kv->dim) a.lanes *= 2;
   a.wide = !((reinterpret_cast<uintptr_t>(a.k) | reinterpret_cast<uintptr_t>(a.v) | a.ldk | a.ldv) & 31);
   const int at_once = kv->n_sm * kRowBlocks;
   a.rows = (a.T + at_once - 1) / at_once;
+  if (turns) {
+    const int vectors = turns * kGatherAhead * (kRowThreads / a.lanes), most = vectors / (2 * kv->heads);
+    a.rows = a.rows > most ? (most > 0 ? most : 1) : a.rows;
+  }
   a.rows = a.rows > kMaxBlockRows ? kMaxBlockRows : a.rows;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((a.T + a.rows - 1) / a.rows);
@@ -496,9 +506,9 @@ int lora_kv_append(lora_kv *kv, int layer, const void *k, int ldk, const void *v
   DeviceGuard g(kv->device);
   const KvSeqs s = seqs_of(page_table, max_pages, seq_lens, row_offsets, n_seqs);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (kv->type == LORA_KV_BF16) return launch_rows(kv_append_kernel<LORA_KV_BF16>, kv, layer, s, a, st);
-  if (kv->type == LORA_KV_E4M3) return launch_rows(kv_append_kernel<LORA_KV_E4M3>, kv, layer, s, a, st);
-  return launch_rows(kv_append_kernel<LORA_KV_INT8>, kv, layer, s, a, st);
+  if (kv->type == LORA_KV_BF16) return launch_rows(kv_append_kernel<LORA_KV_BF16>, kv, layer, s, a, 0, st);
+  if (kv->type == LORA_KV_E4M3) return launch_rows(kv_append_kernel<LORA_KV_E4M3>, kv, layer, s, a, 0, st);
+  return launch_rows(kv_append_kernel<LORA_KV_INT8>, kv, layer, s, a, 0, st);
 }
 
 int lora_kv_gather(lora_kv *kv, int layer, void *k, int ldk, void *v, int ldv, const int32_t *page_table,
@@ -518,9 +528,9 @@ int lora_kv_gather(lora_kv *kv, int layer, void *k, int ldk, void *v, int ldv, c
   DeviceGuard g(kv->device);
   const KvSeqs s = seqs_of(page_table, max_pages, seq_lens, row_offsets, n_seqs);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (kv->type == LORA_KV_BF16) return launch_rows(kv_gather_kernel<LORA_KV_BF16>, kv, layer, s, a, st);
-  if (kv->type == LORA_KV_E4M3) return launch_rows(kv_gather_kernel<LORA_KV_E4M3>, kv, layer, s, a, st);
-  return launch_rows(kv_gather_kernel<LORA_KV_INT8>, kv, layer, s, a, st);
+  if (kv->type == LORA_KV_BF16) return launch_rows(kv_gather_kernel<LORA_KV_BF16>, kv, layer, s, a, kGatherTurns, st);
+  if (kv->type == LORA_KV_E4M3) return launch_rows(kv_gather_kernel<LORA_KV_E4M3>, kv, layer, s, a, kGatherTurns, st);
+  return launch_rows(kv_gather_kernel<LORA_KV_INT8>, kv, layer, s, a, kGatherTurns, st);
 }
 
 size_t lora_attend_workspace_bytes(const lora_kv *kv, int n_heads) {
