@@ -391,15 +391,14 @@ class KvHandle:
 # microseconds on the GPU: their checks read each property of a tensor once.
 
 
-def _rows(t, name: str, device: int, width: int, dtype, where: str, rows: Optional[int] = None):
-    """Address and leading dimension of a [T, ld] operand whose rows of `width` values are reached by its row stride."""
-    shape, stride = t.shape, t.stride()
-    if t.dtype is not dtype or t.get_device() != device or len(shape) != 2 or shape[1] != width or \
-            (stride[1] != 1 and width > 1) or (rows is not None and shape[0] != rows):
-        raise ValueError("%s: %s must be %s [%s, %d] with unit column stride on cuda:%d, not %s %s %s"
-                         % (where, name, dtype, "T" if rows is None else rows, width, device, t.dtype, tuple(shape),
-                            t.device))
-    return t.data_ptr(), stride[0] if shape[0] > 1 else (width + 7) // 8 * 8
+def _rows(t, name: str, device: int, shape, dtype, where: str):
+    """Address and leading dimension of a [T, ld] operand whose rows of shape[1] values are reached by its row stride."""
+    if t.shape == shape and t.is_contiguous() and t.dtype is dtype and t.get_device() == device:
+        return t.data_ptr(), shape[1]
+    if t.dtype is not dtype or t.get_device() != device or t.shape != shape or (t.stride(1) != 1 and shape[1] > 1):
+        raise ValueError("%s: %s must be %s %s with unit column stride on cuda:%d, not %s %s %s"
+                         % (where, name, dtype, list(shape), device, t.dtype, tuple(t.shape), t.device))
+    return t.data_ptr(), t.stride(0) if shape[0] > 1 else (shape[1] + 7) // 8 * 8
 
 
 def _dense(t, name: str, device: int, shape, dtype, where: str) -> int:
@@ -447,15 +446,16 @@ def lora_kv_get_error(kv: KvHandle, stream=None) -> int:
 
 def _kv_rows(fn, where: str, kv: KvHandle, layer: int, k, v, page_table, seq_lens, row_offsets, stream) -> None:
     import torch
-    dev, width, T, n = kv.device, kv.n_kv_heads * kv.head_dim, k.shape[0], seq_lens.shape[0]
-    if page_table.dim() != 2:
+    dev, T, n, paged = kv.device, k.shape[0], seq_lens.shape[0], page_table.shape
+    if len(paged) != 2:
         raise ValueError("%s: page_table must be [n_seqs, max_pages]" % where)
-    kp, ldk = _rows(k, "k", dev, width, torch.bfloat16, where)
-    vp, ldv = _rows(v, "v", dev, width, torch.bfloat16, where, T)
-    table = _dense(page_table, "page_table", dev, (n, page_table.shape[1]), torch.int32, where)
+    shape = (T, kv.n_kv_heads * kv.head_dim)
+    kp, ldk = _rows(k, "k", dev, shape, torch.bfloat16, where)
+    vp, ldv = _rows(v, "v", dev, shape, torch.bfloat16, where)
+    table = _dense(page_table, "page_table", dev, (n, paged[1]), torch.int32, where)
     lens = _dense(seq_lens, "seq_lens", dev, (n,), torch.int32, where)
     off = None if row_offsets is None else _dense(row_offsets, "row_offsets", dev, (n + 1,), torch.int32, where)
-    _check(fn(kv, layer, kp, ldk, vp, ldv, table, page_table.shape[1], lens, off, n, T, _stream_on(stream, dev)), where)
+    _check(fn(kv, layer, kp, ldk, vp, ldv, table, paged[1], lens, off, n, T, _stream_on(stream, dev)), where)
 
 
 def lora_kv_append(kv: KvHandle, layer: int, k, v, page_table, seq_lens, row_offsets=None, stream=None) -> None:
@@ -479,19 +479,21 @@ def lora_attend(kv: KvHandle, layer: int, q, out, page_table, seq_lens, ws, scal
     """Attention of one new token per sequence over the cache: q, out bf16 [n_seqs, n_heads * head_dim]; scale
     1 / sqrt(head_dim) by default; sinks fp32 [n_heads] or None; lse fp32 [n_seqs, n_heads] or None."""
     import torch
-    dev, n, width = kv.device, seq_lens.shape[0], q.shape[-1]
+    dev, n, width, paged = kv.device, seq_lens.shape[0], q.shape[-1], page_table.shape
     where, n_heads = "lora_attend", width // kv.head_dim
-    if width % kv.head_dim or page_table.dim() != 2:
+    if width % kv.head_dim or len(paged) != 2:
         raise ValueError("%s: q must be [n_seqs, n_heads * head_dim], page_table [n_seqs, max_pages]" % where)
-    qp, ldq = _rows(q, "q", dev, width, torch.bfloat16, where, n)
-    op, ldo = _rows(out, "out", dev, width, torch.bfloat16, where, n)
-    table = _dense(page_table, "page_table", dev, (n, page_table.shape[1]), torch.int32, where)
+    shape = (n, width)
+    qp, ldq = _rows(q, "q", dev, shape, torch.bfloat16, where)
+    op, ldo = _rows(out, "out", dev, shape, torch.bfloat16, where)
+    table = _dense(page_table, "page_table", dev, (n, paged[1]), torch.int32, where)
     lens = _dense(seq_lens, "seq_lens", dev, (n,), torch.int32, where)
     sp = None if sinks is None else _dense(sinks, "sinks", dev, (n_heads,), torch.float32, where)
     lp = None if lse is None else _dense(lse, "lse", dev, (n, n_heads), torch.float32, where)
-    wp = _dense(ws, "ws", dev, (ws.numel(),), torch.uint8, where)
-    _check(_lib.lora_attend(kv, layer, qp, ldq, op, ldo, lp, sp, n_heads, table, page_table.shape[1], lens, n,
-                            kv.head_dim ** -0.5 if scale is None else scale, window, wp, ws.numel(),
+    ws_bytes = ws.numel()
+    wp = _dense(ws, "ws", dev, (ws_bytes,), torch.uint8, where)
+    _check(_lib.lora_attend(kv, layer, qp, ldq, op, ldo, lp, sp, n_heads, table, paged[1], lens, n,
+                            kv.head_dim ** -0.5 if scale is None else scale, window, wp, ws_bytes,
                             _stream_on(stream, dev)), where)
 
 
@@ -500,25 +502,27 @@ def lora_rmsnorm(x, weight, eps: float, residual=None, residual_out=None, y=None
     """h = x + residual and its root-mean-square norm: h to residual_out, the norm to y (bf16) and / or q
     (float8_e4m3fn) with q_scales fp32 [T] (one per row) or [T, d / group]."""
     import torch
-    where, dev, (T, d), bf16 = "lora_rmsnorm", x.get_device(), x.shape, torch.bfloat16
-    xp, ldx = _rows(x, "x", dev, d, bf16, where)
+    where, dev, shape, bf16 = "lora_rmsnorm", x.get_device(), x.shape, torch.bfloat16
+    T, d = shape
+    xp, ldx = _rows(x, "x", dev, shape, bf16, where)
     wp = _dense(weight, "weight", dev, (d,), bf16, where)
     rp = op = yp = qp = None
     ldr = ldo = ldy = ldq = 0
     if residual is not None:
-        rp, ldr = _rows(residual, "residual", dev, d, bf16, where, T)
+        rp, ldr = _rows(residual, "residual", dev, shape, bf16, where)
     if residual_out is not None:
-        op, ldo = _rows(residual_out, "residual_out", dev, d, bf16, where, T)
+        op, ldo = _rows(residual_out, "residual_out", dev, shape, bf16, where)
     if y is not None:
-        yp, ldy = _rows(y, "y", dev, d, bf16, where, T)
+        yp, ldy = _rows(y, "y", dev, shape, bf16, where)
     if q is not None:
-        qp, ldq = _rows(q, "q", dev, d, torch.float8_e4m3fn, where, T)
+        qp, ldq = _rows(q, "q", dev, shape, torch.float8_e4m3fn, where)
     group, sp = 0, None
     if q is not None:
         if q_scales is None:
             raise ValueError("%s: q needs q_scales" % where)
-        if q_scales.dim() == 2:
-            n = q_scales.shape[1]
+        grid = q_scales.shape
+        if len(grid) == 2:
+            n = grid[1]
             if n < 1 or d % n:
                 raise ValueError("%s: q_scales must be [T] or [T, d / group]" % where)
             group = d // n if n > 1 else 0
