@@ -11,8 +11,8 @@
 //
 // Bound by HBM: 4 flops per cached element and query head, at most 16 query
 // heads to a byte.  (64 requests of 200 to 4000 tokens, bf16, 32 heads of 128: 1.15 GB
-// in 184 us, 6.3 TB/s; 512 of 64 to 2048, e4m3, 32 / 8 heads: 585 MB in 111 us, 5.2 TB/s.
-// Short calls are latency: 16 requests of up to 100 tokens 10 us.)  So the split is by bytes, evenly, whatever the lengths:
+// in 182 us, 6.3 TB/s; 512 of 64 to 2048, e4m3, 32 / 8 heads: 585 MB in 110 us, 5.3 TB/s.
+// Short calls are latency: 16 requests of up to 100 tokens 9 us.)  So the split is by bytes, evenly, whatever the lengths:
 //  - The batch is one flat list of slots, ordered by (sequence, unit, step).  A
 //    unit is one key head with up to 8 (or 16) of its query heads; a step is 16
 //    TT consecutive tokens of it.  A unit has one slot for each step and one
@@ -341,9 +341,11 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(KvView kv, KvSeqs
   constexpr int kCountAt = 42;
   long long mine = 0;
   unsigned longest = 0;
+  int last_len = 0;
 #pragma unroll 1
   for (int i = s0; i < s1; ++i) {
-    const unsigned n = unit_slots(seq_len(kv, s, i), a.window, TT);
+    last_len = seq_len(kv, s, i);
+    const unsigned n = unit_slots(last_len, a.window, TT);
     mine += n | (n ? 1ll << kCountAt : 0);
     longest = max(longest, n);
   }
@@ -367,7 +369,9 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(KvView kv, KvSeqs
     }
   constexpr long long kSlotBits = (1ll << kCountAt) - 1;
   long long *prefix = reinterpret_cast<long long *>(smem);  // [threads], before the rings are in use
+  int *only = reinterpret_cast<int *>(prefix + blockDim.x);  // lengths, where a thread has one sequence
   prefix[tid] = before - mine;
+  only[tid] = last_len;
   __syncthreads();
 
   // The sequence at place y of the list of slots (or of sequences with a token),
@@ -378,6 +382,12 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(KvView kv, KvSeqs
     int t = __popc(__ballot_sync(~0u, key(prefix[lane * n_warps]) <= y)) - 1;
     t = t * n_warps + __popc(__ballot_sync(~0u, lane < n_warps && key(prefix[min(t * n_warps + lane, (int)blockDim.x - 1)]) <= y)) - 1;
     long long sum = prefix[t];
+    if (per == 1) {  // (the usual case: at most as many sequences as threads)
+      seq = t;
+      len = only[t];
+      before = sum & kSlotBits;
+      return;
+    }
     const int end = min(s.n, (t + 1) * per);
 #pragma unroll 1
     for (int i0 = t * per; i0 < end; i0 += 32) {
