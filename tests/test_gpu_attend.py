@@ -369,3 +369,16 @@ def test_one_workspace_for_caches_and_graphs_in_turn(cuda_device):
     finally:
         for c in caches:
             c.__exit__()
+
+
+@pytest.mark.parametrize("kv_type", list(R.TYPES))
+@pytest.mark.parametrize("heads,kv_heads,dim,page,lens", [(8, 2, 64, 64, [30000, 7, 20011]), (1, 1, 128, 16, [40000]),
+                                                          (16, 1, 256, 32, [9000, 1, 5000]), (40, 5, 80, 16, [7777] * 3)])
+def test_units_cut_over_many_blocks(cuda_device, kv_type, heads, kv_heads, dim, page, lens):
+    """Joins of many parts, of two units in one block, and of fewer rows than threads."""
+    b = R.Batch(lens, kv_heads, dim, page, seed=17)
+    q = queries(b, heads, 17)
+    with Cache(b, kv_type, cuda_device) as c:
+        c.append()
+        check(c, kv_type, q, *attend(c, q))
+        check(c, kv_type, q, *attend(c, q, window=4097), window=4097)
