@@ -111,6 +111,7 @@ _sig("lora_kv_gather", _I, [_P, _I, _P, _I, _P, _I, _P, _I, _P, _P, _I, _I, _P])
 _sig("lora_attend_workspace_bytes", _Z, [_P, _I])
 _sig("lora_attend", _I, [_P, _I, _P, _I, _P, _I, _P, _P, _I, _P, _I, _P, _I, ctypes.c_float, _I, _P, _Z, _P])
 _sig("lora_selftest_stalled_attend", _I, [_P, _I, _P, _I, _P, _I, _I, _P, _I, _P, _I, _P, _Z, _P])
+_sig("lora_selftest_late_lane_attend", _I, [_P, _I, _P, _I, _P, _I, _I, _P, _I, _P, _I, _P, _Z, _I, _P])
 _sig("lora_rmsnorm", _I, [_I, _P, _I, _P, _I, _P, _I, _P, ctypes.c_float, _P, _I, _P, _I, _P, _I, _I, _I, _P])
 _sig("lora_get_error", _I, [_P, ctypes.POINTER(_I), _P])
 _sig("lora_kernel_launches", ctypes.c_uint64, [])
@@ -563,3 +564,12 @@ def lora_selftest_stalled_attend(kv: KvHandle, layer: int, q, out, page_table, s
                                              q.shape[1] // kv.head_dim, page_table.data_ptr(), page_table.shape[1],
                                              seq_lens.data_ptr(), seq_lens.shape[0], ws.data_ptr(), ws.numel(),
                                              _stream_on(stream, kv.device)), "lora_selftest_stalled_attend")
+
+
+def lora_selftest_late_lane_attend(kv: KvHandle, layer: int, q, out, page_table, seq_lens, ws, lane: int, stream=None) -> None:
+    """Test only: lora_attend (scale 1) whose warps' lane `lane` finds its waits run out
+    from the third step on (LORA_ERR_TIMEOUT in the cache's sticky status)."""
+    _check(_lib.lora_selftest_late_lane_attend(kv, layer, q.data_ptr(), q.stride(0), out.data_ptr(), out.stride(0),
+                                               q.shape[1] // kv.head_dim, page_table.data_ptr(), page_table.shape[1],
+                                               seq_lens.data_ptr(), seq_lens.shape[0], ws.data_ptr(), ws.numel(), lane,
+                                               _stream_on(stream, kv.device)), "lora_selftest_late_lane_attend")

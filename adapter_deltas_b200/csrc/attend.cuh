@@ -70,7 +70,7 @@ struct AttendArgs {
   float scale2;        // scale * log2(e)
   int window;
   int n_stages;
-  int stall;           // test only: nothing is fetched, so that every wait runs out
+  int stall;           // test only: kStallAll, or kStallLane + a lane
   unsigned long long wait_ns;
   // workspace: what each block's borders cut
   unsigned long long *done;  // [blocks] how many blocks of the unit that starts in a block and goes on are done
@@ -524,7 +524,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(KvView kv, KvSeqs
       if (TT > 1 && !one_copy) n = __popc(__ballot_sync(~0u, copy));
       if (lane == 0) {
         if (fnew) held[warp][stage] = {fseq, pack_unit(fkvh, fh0), fpos, flen};
-        if (!a.stall) mbar_arrive_expect_tx(&full[warp][stage], n * tile_bytes);
+        if (a.stall != kStallAll) mbar_arrive_expect_tx(&full[warp][stage], n * tile_bytes);
       }
       if (n < t1 - t0) {
         const unsigned ok = TT > 1 && !one_copy ? __ballot_sync(~0u, copy) << t0 : 0u;
@@ -532,7 +532,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(KvView kv, KvSeqs
         if (lane == 0) set_status(kv.status, LORA_ERR_BAD_ID);
       }
       __syncwarp();
-      if (copy && !a.stall)
+      if (copy && a.stall != kStallAll)
         bulk_g2s(ring + stage * stage_bytes + tile * tile_bytes, fhead + at, one_copy ? n * tile_bytes : tile_bytes,
                  &full[warp][stage]);
       fpos += kStep;
@@ -764,11 +764,18 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(KvView kv, KvSeqs
             for (int x = lane * 128; x < bytes; x += 32 * 128) asm volatile("prefetch.global.L1 [%0];" ::"l"(q + x));
         }
       }
-      if (!mbar_wait_bounded(&full[warp][stage], phase, kv.status, a.wait_ns)) {
+      // One verdict a warp: its lanes read their clocks one by one, and where a copy
+      // lands as the limit passes, some see it and others do not.
+      bool landed = mbar_wait_bounded(&full[warp][stage], phase, kv.status, a.wait_ns);
+      if (a.stall == kStallLane + lane && i >= 2) landed = false;
+      if (!__all_sync(~0u, landed)) {
         // copies in flight must land before the block ends (again a bounded wait)
 #pragma unroll 1
         for (int k = 0; k < a.n_stages; ++k) (void)mbar_wait_bounded(&full[warp][k], phase ^ (k < stage), kv.status, a.wait_ns);
-        if (lane == 0) dead_block = 1;
+        if (lane == 0) {
+          dead_block = 1;
+          set_status(kv.status, LORA_ERR_TIMEOUT);
+        }
         break;
       }
       const uint32_t st32 = ring32 + stage * stage_bytes;

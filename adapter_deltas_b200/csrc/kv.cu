@@ -551,7 +551,16 @@ int lora_selftest_stalled_attend(lora_kv *kv, int layer, const void *q, int ldq,
                                  size_t ws_bytes, void *stream) {
   NvtxRange nvtx_range("lora_selftest_stalled_attend");
   return attend(kv, layer, q, ldq, out, ldo, nullptr, nullptr, n_heads, page_table, max_pages, seq_lens, n_seqs, 1.f, 0,
-                ws, ws_bytes, 1, stream);
+                ws, ws_bytes, kStallAll, stream);
+}
+
+int lora_selftest_late_lane_attend(lora_kv *kv, int layer, const void *q, int ldq, void *out, int ldo, int n_heads,
+                                   const int32_t *page_table, int max_pages, const int32_t *seq_lens, int n_seqs, void *ws,
+                                   size_t ws_bytes, int lane, void *stream) {
+  NvtxRange nvtx_range("lora_selftest_late_lane_attend");
+  if (lane < 0 || lane > 31) return LORA_ERR_INVALID_ARG;
+  return attend(kv, layer, q, ldq, out, ldo, nullptr, nullptr, n_heads, page_table, max_pages, seq_lens, n_seqs, 1.f, 0,
+                ws, ws_bytes, kStallLane + lane, stream);
 }
 
 }  // extern "C"

@@ -233,6 +233,10 @@ inline int cuda_status(cudaError_t e) {
 }
 
 int attend_setup(lora_kv *kv);
+// What the self-tests stall: nothing is fetched, so that every wait runs out; or one
+// lane of each warp finds its waits run out from the warp's third step on.
+enum { kStallAll = 1, kStallLane = 2 };
+
 struct AttendCall {
   const void *q;
   int ldq;
@@ -244,7 +248,7 @@ struct AttendCall {
   float scale;
   int window;
   void *ws;
-  int stall;  // test only
+  int stall;  // test only: 0, kStallAll, or kStallLane + a lane
 };
 int launch_attend(const lora_kv *kv, int layer, const KvSeqs &s, const AttendCall &c, cudaStream_t st);
 size_t attend_workspace_bytes(const lora_kv *kv, int n_heads);

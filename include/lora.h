@@ -733,6 +733,17 @@ LORA_API int lora_selftest_stalled_attend(lora_kv *kv, int layer, const void *q,
                                  const int32_t *page_table, int max_pages, const int32_t *seq_lens, int n_seqs, void *ws,
                                  size_t ws_bytes, void *stream);
 
+/*
+ * Test only: the same call with everything fetched, but from a warp's third
+ * step on one lane (0..31) finds its waits run out while the others' data
+ * arrive.  The whole warp then gives up: the launch completes, lora_kv_get_error
+ * reads LORA_ERR_TIMEOUT, each row is either as it was or as lora_attend
+ * leaves it (scale 1), and the cache and the workspace stay usable.
+ */
+LORA_API int lora_selftest_late_lane_attend(lora_kv *kv, int layer, const void *q, int ldq, void *out, int ldo, int n_heads,
+                                   const int32_t *page_table, int max_pages, const int32_t *seq_lens, int n_seqs, void *ws,
+                                   size_t ws_bytes, int lane, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
