@@ -53,7 +53,7 @@ namespace lora {
 constexpr int kAttMaxWarps = 12;
 constexpr int kAttMaxStages = 8;
 constexpr int kAttSmem = 227 * 1024;
-constexpr int kSlack = 4, kVSlack = 2;  // powers of two
+constexpr int kSlack = 4, kWeight = 11;  // powers of two (kWeight + kSlack: within fp16)
 constexpr int kCutSteps = 3;
 constexpr int kMaxSlotsLog2 = 30;  // of a block: counted in 32 bits
 
@@ -112,10 +112,15 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-__device__ constexpr float exp2_int(int e) { return (float)(1 << e); }
 __device__ __forceinline__ float exp2_fast(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+__device__ __forceinline__ float log2_fast(float x) {  // (0: minus infinity)
+  float r;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
 
@@ -583,7 +588,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(KvView kv, KvSeqs
     uint32_t qa[NT][QN];
     float qs[NT][2];  // what a score is multiplied by: the softmax's scale and that of q's terms
     float o[NT][NB][4], m[NT][2], l[NT][2];
-    float vtop = 0.f, unit = 0.f;  // (8 bits) V's scales: reference, and the weights' unit by it
+    float w[NT][2];  // (8 bits) reference of the weights times V's scales
     int cseq = -1, cunit = -1, cpos = 0, clen = 0, cfirst = 0;  // of the step to compute; cfirst: the unit's first token
     bool cut_before = false, cnew = true;
     int stage = 0, fstage = 0;
@@ -680,7 +685,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(KvView kv, KvSeqs
           }
 #pragma unroll
           for (int h = 0; h < NT; ++h) {
-            float mul[2];
+            float mul[2], half[2];  // (8 bits: 2^(w - m), which may pass the exponent's range, in two halves)
             bool on[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
@@ -689,7 +694,8 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(KvView kv, KvSeqs
               l[h][e] += __shfl_xor_sync(~0u, l[h][e], 16);
               const int r = 8 * h + j2 + e, hd = kvh * a.group + h0 + r;
               on[e] = r < a.rows && h0 + r < a.group;
-              mul[e] = TYPE == LORA_KV_BF16 ? 1.f : vtop / exp2_int(15 - kSlack - kVSlack);
+              half[e] = TYPE == LORA_KV_BF16 ? 1.f : w[h][e] == -INFINITY ? 0.f : exp2_fast(0.5f * (w[h][e] - m[h][e]));
+              mul[e] = half[e];
               if (!on[e]) continue;
               if (whole) {
                 const Ends x = finish(a.sinks, hd, m[h][e], l[h][e]);
@@ -713,6 +719,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(KvView kv, KvSeqs
                 const float got = __shfl_xor_sync(~0u, g & 1 ? x.x : x.y, 4);
                 x = g & 1 ? make_float2(got, x.y) : make_float2(x.x, got);
               }
+              if (TYPE != LORA_KV_BF16) x = make_float2(x.x * half[e], x.y * half[e]);
               return make_float2(x.x * mul[e], x.y * mul[e]);
             };
             if (whole) {
@@ -747,11 +754,11 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(KvView kv, KvSeqs
 #pragma unroll
         for (int h = 0; h < NT; ++h) {
           m[h][0] = m[h][1] = -INFINITY;
+          w[h][0] = w[h][1] = -INFINITY;
           l[h][0] = l[h][1] = 0.f;
 #pragma unroll
           for (int b = 0; b < NB; ++b) o[h][b][0] = o[h][b][1] = o[h][b][2] = o[h][b][3] = 0.f;
         }
-        vtop = unit = 0.f;
         load_q();
         {  // the next unit's q, towards this SM: the rows behind, or the next sequence's first
           const int kvh = unit_kvh(cunit), h0 = unit_h0(cunit);
@@ -864,13 +871,13 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(KvView kv, KvSeqs
       }
 
       // ---- weights
-      float vs[TT][2];
+      float lv[TT][2];  // log2 of V's scales
       if (TYPE != LORA_KV_BF16) {
 #pragma unroll
         for (int t = 0; t < TT; ++t) {
           const uint8_t *sc = stp + t * tile_bytes + 2 * kTileTokens * row_bytes + kTileTokens * 4;
-          vs[t][0] = *reinterpret_cast<const float *>(sc + g * 4);
-          vs[t][1] = *reinterpret_cast<const float *>(sc + g * 4 + 32);
+          lv[t][0] = log2_fast(*reinterpret_cast<const float *>(sc + g * 4));
+          lv[t][1] = log2_fast(*reinterpret_cast<const float *>(sc + g * 4 + 32));
         }
       }
       if (partial) {
@@ -882,54 +889,52 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(KvView kv, KvSeqs
             if (j < lo || j >= hi || (bad >> t & 1)) {
 #pragma unroll
               for (int h = 0; h < NT; ++h) c[t][h][2 * e] = c[t][h][2 * e + 1] = -INFINITY;
-              if (TYPE != LORA_KV_BF16) vs[t][e] = 0.f;
+              if (TYPE != LORA_KV_BF16) lv[t][e] = -INFINITY;
             }
           }
       }
       // m is a reference, within 2^kSlack of the running maximum: while no
-      // score passes it by more, nothing is exchanged and nothing rescaled.
-      // V's scales likewise have vtop, within 2^kVSlack of the largest so far.
-      float mx[NT][2], vm = 0.f;
+      // score passes it by more, nothing is exchanged and nothing rescaled.  The
+      // values' sums have one of their own: with 8 bits w, by the weights times V's
+      // scales (in logarithms: their product may pass the exponent's range), which
+      // leaves the largest of those between 2^kWeight and 2^(kWeight + kSlack).
+      // (By V's largest scale alone a token with a far larger V and next to no
+      // weight would take the others' bits.)
+      float mx[NT][2], wx[NT][2];
       bool moved = false;
 #pragma unroll
       for (int h = 0; h < NT; ++h)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           mx[h][e] = c[0][h][e];
+          wx[h][e] = -INFINITY;
 #pragma unroll
-          for (int t = 0; t < TT; ++t) mx[h][e] = fmaxf(mx[h][e], fmaxf(c[t][h][e], c[t][h][e + 2]));
-          moved |= mx[h][e] > m[h][e] + kSlack;
-        }
-      if (TYPE != LORA_KV_BF16) {
-#pragma unroll
-        for (int t = 0; t < TT; ++t) vm = fmaxf(vm, fmaxf(vs[t][0], vs[t][1]));
-        moved |= vm > vtop * (1 << kVSlack);
-      }
-      if (__any_sync(~0u, moved)) {
-        float fade = 1.f;
-        if (TYPE != LORA_KV_BF16) {
-          vm = fmaxf(vm, __shfl_xor_sync(~0u, vm, 4));
-          vm = fmaxf(vm, __shfl_xor_sync(~0u, vm, 8));
-          vm = fmaxf(vm, __shfl_xor_sync(~0u, vm, 16));
-          if (vm > vtop) {
-            fade = __fdividef(vtop, vm);
-            vtop = vm;
-            unit = exp2_int(15 - kSlack - kVSlack) / vtop;
+          for (int t = 0; t < TT; ++t) {
+            mx[h][e] = fmaxf(mx[h][e], fmaxf(c[t][h][e], c[t][h][e + 2]));
+            if (TYPE != LORA_KV_BF16) wx[h][e] = fmaxf(wx[h][e], fmaxf(c[t][h][e] + lv[t][0], c[t][h][e + 2] + lv[t][1]));
           }
+          moved |= mx[h][e] > m[h][e] + kSlack;
+          if (TYPE != LORA_KV_BF16) moved |= wx[h][e] > w[h][e] + (kWeight + kSlack);
         }
+      if (__any_sync(~0u, moved)) {
 #pragma unroll
         for (int h = 0; h < NT; ++h)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float x = mx[h][e];
-            x = fmaxf(x, __shfl_xor_sync(~0u, x, 4));
-            x = fmaxf(x, __shfl_xor_sync(~0u, x, 8));
-            x = fmaxf(x, __shfl_xor_sync(~0u, x, 16));
-            x = fmaxf(x, m[h][e]);
-            float alpha = exp2_fast(m[h][e] - (x == -INFINITY ? 0.f : x));
+            auto highest = [&](float x) {
+              x = fmaxf(x, __shfl_xor_sync(~0u, x, 4));
+              x = fmaxf(x, __shfl_xor_sync(~0u, x, 8));
+              return fmaxf(x, __shfl_xor_sync(~0u, x, 16));
+            };
+            auto raise = [](float &to, float x) {  // returns what was summed by the old one is worth
+              x = fmaxf(x, to);
+              const float alpha = exp2_fast(to - (x == -INFINITY ? 0.f : x));
+              to = x;
+              return alpha;
+            };
+            float alpha = raise(m[h][e], highest(mx[h][e]));
             l[h][e] *= alpha;
-            m[h][e] = x;
-            alpha *= fade;
+            if (TYPE != LORA_KV_BF16) alpha = raise(w[h][e], highest(wx[h][e]) - kWeight);
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
               if (ANY && b >= nb) continue;
@@ -941,14 +946,15 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(KvView kv, KvSeqs
       // bf16: the weights as two terms, hi with the type's leading bits (cut, so
       // that the rest is exact) and the rest's leading bits: one term would add an
       // error of the size of the result's own rounding.  8 bits: the weights times
-      // V's scales as fp16, whose 11 bits leave a fraction of that; in units
-      // such that none overflows (2^9 over vtop), what is below 2^-34 of the largest
-      // is lost.  Each turned: a thread then has two tokens of head g.
+      // V's scales as fp16, whose 11 bits leave a fraction of that; the largest is
+      // 2^kWeight or more, so that one is off by at most 2^-11 of itself or 2^-36 of
+      // the largest.  Each turned: a thread then has two tokens of head g.
       constexpr int TERMS = TYPE == LORA_KV_BF16 ? 2 : 1;
       uint32_t pw[TERMS][TT][NT][2];
 #pragma unroll
       for (int h = 0; h < NT; ++h) {
         const float base[2] = {m[h][0] == -INFINITY ? 0.f : m[h][0], m[h][1] == -INFINITY ? 0.f : m[h][1]};
+        const float wbase[2] = {w[h][0] == -INFINITY ? 0.f : w[h][0], w[h][1] == -INFINITY ? 0.f : w[h][1]};
 #pragma unroll
         for (int t = 0; t < TT; ++t)
 #pragma unroll
@@ -961,8 +967,8 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(KvView kv, KvSeqs
               pw[0][t][h][e] = turn(hi2);
               pw[TERMS - 1][t][h][e] = turn(pack_bf16x2(p0 - bf16_lo(hi2), p1 - bf16_hi(hi2)));
             } else {
-              const float w = vs[t][e] * unit;
-              pw[0][t][h][e] = turn(pack_f16x2(p0 * w, p1 * w));
+              pw[0][t][h][e] = turn(pack_f16x2(exp2_fast(c[t][h][2 * e] + lv[t][e] - wbase[0]),
+                                               exp2_fast(c[t][h][2 * e + 1] + lv[t][e] - wbase[1])));
             }
           }
       }

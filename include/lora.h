@@ -640,7 +640,10 @@ LORA_API size_t lora_attend_workspace_bytes(const lora_kv *kv, int n_heads);
  *   ws, ws_bytes device workspace of lora_attend_workspace_bytes, 16-byte
  *                aligned; its content need not survive between calls, and calls
  *                that may overlap on the GPU need one each
- * fp32 accumulation and statistics; out is rounded once.  A sequence of length
+ * Scores, statistics and sums are fp32; out is rounded once.  The weights that
+ * multiply V are rounded: over a bf16 cache to 16 bits; over an 8-bit cache,
+ * times V's scale, to fp16 (2^-11 of itself, or 2^-36 of the head's largest such
+ * product).  A sequence of length
  * 0 gets zeros (lse: its sink, or minus infinity), one of length -1 keeps its
  * rows as they were, and so does one whose length is below -1 or past
  * max_pages, which raises the sticky LORA_ERR_BAD_ID.  So does a batch of more

@@ -1,0 +1,131 @@
+"""Attention over caches whose rows differ widely in magnitude.
+
+Every row of an 8-bit cache has its own scale, so rows of 2^-100 and of 2^100 may
+lie side by side, and how large a row is says nothing about how much weight its
+token gets.  The results are held to bounds that follow the terms which count:
+
+  - a score is off by err_s as kv_reference.attend derives it; a weight by twice
+    that relatively, plus 2^-15 for the exponential and the running rescale, plus
+    len * 2^-23 for the sums;
+  - 8-bit caches round a weight times its row's scale to fp16, 2^-11 relative; its
+    exponent is a sum of the score s in base 2 and the scale's logarithm, two
+    roundings of up to 2^-24 (|s| + 128) each and 2^-22 * 128 of the logarithm, times
+    ln 2;
+  - such a product is held in units in which the largest of them is at least 2^11,
+    so that fp16's half smallest step 2^-25 is at most 2^-36 of the largest, for each
+    of len tokens, times the largest code;
+  - the result is rounded to bf16 once (2^-8; 2^-134 below its normal range).
+"""
+
+import math
+
+import pytest
+import torch
+
+import kv_reference as R
+from test_gpu_attend import attend, queries
+from test_gpu_kv import Cache
+
+pytestmark = pytest.mark.gpu
+
+
+def expected(q, k, v, kv_type, scale, window=0):
+    """One sequence's result [heads, dim] and what it may be off by."""
+    heads, dim = q.shape
+    if window and len(k) > window:
+        k, v = k[-window:], v[-window:]
+    n, kv_heads = len(k), k.shape[1]
+    kx, (code, u) = R.values(k, kv_type).transpose(0, 1), R.held(v, kv_type)
+    vx = (code * u[..., None]).transpose(0, 1)
+    qx = q.double().view(kv_heads, -1, dim)
+    s = scale * qx @ kx.transpose(1, 2)
+    mag = (scale * qx.abs() @ kx.abs().transpose(1, 2)).amax(-1)
+    p = torch.softmax(s, -1)
+    out, spread = p @ vx, p @ vx.abs()
+    rel = 2 * mag * (dim + 4) * 2.0 ** -23 + 2.0 ** -15 + n * 2.0 ** -23
+    floor = torch.zeros_like(rel)
+    if kv_type != "bf16":
+        s2 = (mag * math.log2(math.e) + 128)
+        rel = rel + 2.0 ** -11 + math.log(2) * (2 * 2.0 ** -24 * s2 + 2.0 ** -22 * 128)
+        top = (p * u.transpose(0, 1)[:, None]).amax(-1)
+        floor = n * 2.0 ** -36 * R.QMAX[kv_type] * top
+    tol = R.U_BF16 * out.abs() + (rel[..., None] * spread + floor[..., None]) * (1 + R.U_BF16) + 2.0 ** -134
+    return out.reshape(heads, dim), tol.reshape(heads, dim)
+
+
+def hold(b, kv_type, q, out, window=0):
+    for i, n in enumerate(b.lens):
+        want, tol = expected(q[i].view(-1, b.dim), b.k[i], b.v[i], kv_type, b.dim ** -0.5, window)
+        got = out[i].view(-1, b.dim).double()
+        off = ((got - want).abs() / tol).max() if torch.isfinite(got).all() else float("nan")
+        assert off <= 1, "sequence %d of length %d: %s of what it may be off" % (i, n, off)
+
+
+def gains(n, way):
+    """Powers of two (nearly) that the V rows of n tokens are multiplied by."""
+    x = torch.linspace(0, 1, n) if n > 1 else torch.zeros(1)
+    if way == "grow":
+        return torch.exp2(60 * x - 30)
+    if way == "shrink":
+        return torch.exp2(30 - 60 * x)
+    g = torch.Generator().manual_seed(n)
+    steps = torch.tensor([1.0, 5.0, 100.0, 2.0 ** 20, 2.0 ** -20, 2.0 ** -40])
+    if way == "jump":
+        return steps[torch.randint(len(steps), (n,), generator=g)]
+    return steps[torch.randint(len(steps), (n // 50 + 1,), generator=g)].repeat_interleave(50)[:n]  # "levels"
+
+
+LENS = [[512, 1, 17, 300, 64], [30000, 7]]
+
+
+@pytest.mark.parametrize("kv_type", list(R.TYPES))
+@pytest.mark.parametrize("way", ["grow", "shrink", "jump", "levels"])
+@pytest.mark.parametrize("lens", LENS)
+@pytest.mark.parametrize("heads,kv_heads,dim", [(8, 2, 64), (4, 4, 128), (16, 1, 256), (20, 2, 48)])
+def test_values_that_grow_shrink_and_jump(cuda_device, kv_type, way, lens, heads, kv_heads, dim):
+    b = R.Batch(lens, kv_heads, dim, 32, seed=31)
+    for v in b.v:
+        v.copy_((v.float() * gains(len(v), way)[:, None, None]).to(torch.bfloat16))
+    q = queries(b, heads, 31)
+    with Cache(b, kv_type, cuda_device) as c:
+        c.append()
+        hold(b, kv_type, q, attend(c, q)[0])
+        hold(b, kv_type, q, attend(c, q, window=100)[0], window=100)
+        assert c.error() == 0
+
+
+@pytest.mark.parametrize("kv_type", list(R.TYPES))
+@pytest.mark.parametrize("spread", [8, 20, 26, 30, 34, 60, 100])
+@pytest.mark.parametrize("lens,at", [([512, 90], 3), ([512, 90], 70), ([30000, 500], 5), ([30000, 500], 499)])
+def test_a_large_value_without_weight(cuda_device, kv_type, spread, lens, at):
+    """One token has V 2^spread times the others' and a score far below theirs: nothing of it is to be seen."""
+    b = R.Batch(lens, 2, 64, 16, seed=32)
+    q = queries(b, 8, 32)
+    g = q.view(len(lens), 2, 4, 64)
+    g.copy_(g[:, :, :1] + 0.1 * g)  # the heads of a key head look the same way
+    for i in range(len(lens)):
+        mean = g[i].float().mean(1)  # [kv_heads, dim]
+        b.k[i][at] = (-mean / mean.square().sum(-1, keepdim=True) * 200 * 8).to(torch.bfloat16)  # score about -200
+        b.v[i][at] *= 2.0 ** spread
+    with Cache(b, kv_type, cuda_device) as c:
+        c.append()
+        hold(b, kv_type, q, attend(c, q)[0])
+
+
+@pytest.mark.parametrize("kv_type", ["e4m3", "int8"])
+def test_small_and_no_values(cuda_device, kv_type):
+    """Rows of zeros hold the largest weights, and what is left is near the end of the types' ranges."""
+    b = R.Batch([400, 33, 20000], 2, 64, 16, seed=33)
+    for v in b.v:
+        v[::2] = 0
+        v[1::2] = (v[1::2].float() * 2.0 ** -96).to(torch.bfloat16)
+    q = queries(b, 8, 33, gain=4.0)
+    with Cache(b, kv_type, cuda_device) as c:
+        c.append()
+        hold(b, kv_type, q, attend(c, q)[0])
+    for v in b.v:
+        v.zero_()
+    with Cache(b, kv_type, cuda_device) as c:
+        c.append()
+        out, lse = attend(c, q)
+        assert (out == 0).all() and torch.isfinite(lse).all()
