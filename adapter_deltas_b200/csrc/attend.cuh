@@ -212,14 +212,11 @@ struct Ends {
 };
 __device__ __forceinline__ Ends finish(const float *sinks, int head, float m, float l) {
   Ends e;
-  float base = m;
-  if (sinks) {
-    const float sink = sinks[head] * 1.44269504f;
-    base = fmaxf(m, sink);
-    l = l * exp2_fast(m - base) + exp2_fast(sink - base);
-  }
-  e.mul = __fdividef(exp2_fast(m - base), l);
-  if (m == -INFINITY && !sinks) e.mul = __int_as_float(0x7fc00000);  // (every score minus infinity: 0 / 0)
+  const float sink = sinks ? sinks[head] * 1.44269504f : -INFINITY;
+  float base = fmaxf(m, sink);
+  base = base == -INFINITY ? 0.f : base;
+  if (sinks) l = l * exp2_fast(m - base) + exp2_fast(sink - base);
+  e.mul = l == 0.f ? 0.f : __fdividef(exp2_fast(m - base), l);  // (nothing has any weight: zeros, as without a token)
   e.lse = fmaf(base, 0.693147181f, 0.693147181f * __log2f(l));
   return e;
 }

@@ -649,7 +649,8 @@ LORA_API size_t lora_attend_workspace_bytes(const lora_kv *kv, int n_heads);
  * max_pages, which raises the sticky LORA_ERR_BAD_ID.  So does a batch of more
  * than 2^30 steps for each SM (a step is 16 to 64 tokens of a key head; minutes of
  * work), of which no row with a token is written.  Tokens on a page
- * outside [0, n_pages) are left out of the sums and raise it too.  The result
+ * outside [0, n_pages) are left out of the sums and raise it too; where that
+ * leaves none, or all scores are minus infinity, the row is as for length 0.  The result
  * does not depend on what the pages hold past a sequence's end or before its
  * window.  Equal inputs give equal bits.
  */
