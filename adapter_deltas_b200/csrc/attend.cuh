@@ -773,9 +773,20 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(KvView kv, KvSeqs
       bool landed = mbar_wait_bounded(&full[warp][stage], phase, kv.status, a.wait_ns);
       if (a.stall == kStallLane + lane && i >= 2) landed = false;
       if (!__all_sync(~0u, landed)) {
-        // copies in flight must land before the block ends (again a bounded wait)
+        // Copies in flight (steps fetched and not computed) must land before the block
+        // ends: they get the limit once more, all together.
+        const long long t0 = clock64();
+        const int flying = a.stall == kStallAll ? 0 : fetched - i;
 #pragma unroll 1
-        for (int k = 0; k < a.n_stages; ++k) (void)mbar_wait_bounded(&full[warp][k], phase ^ (k < stage), kv.status, a.wait_ns);
+        for (int k = 0; k < flying; ++k) {
+          const long long spent = (clock64() - t0) / 2;  // (ns at 2 GHz, as the wait counts them)
+          (void)mbar_wait_bounded(&full[warp][stage], phase, kv.status, max((long long)a.wait_ns - spent, 0ll));
+          if (++stage == a.n_stages) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+        __syncwarp();
         if (lane == 0) {
           dead_block = 1;
           set_status(kv.status, LORA_ERR_TIMEOUT);

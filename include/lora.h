@@ -706,7 +706,8 @@ LORA_API uint64_t lora_kernel_launches(void);
 /*
  * Wall-clock limit of the decode and attention kernels' bounded waits (for a
  * stage of a copy ring), in nanoseconds, for the launches that follow; 0
- * restores the default of one second.  A wait that runs out sets
+ * restores the default of one second (copies that are in flight when a wait
+ * runs out get as long again, together).  A wait that runs out sets
  * LORA_ERR_TIMEOUT in the pool's (or cache's) sticky status, leaves the
  * rows that needed the data untouched and lets the kernel finish; it never
  * faults.  Tests lower it to reach that path quickly.

@@ -52,3 +52,31 @@ def test_late_lane_refusals(cuda_device):
                 L.lora_selftest_late_lane_attend(c.kv, 0, q, torch.empty_like(q), c.table, c.lens, ws, lane)
             assert e.value.code == L.LORA_ERR_INVALID_ARG
         assert L.lora_kernel_launches() == n
+
+
+@pytest.mark.parametrize("kv_type,dim", [("bf16", 16), ("e4m3", 16), ("int8", 64), ("bf16", 256)])
+def test_giving_up_takes_one_limit(cuda_device, kv_type, dim):
+    """Nothing is fetched, so nothing is in flight: a launch that gives up ends after one limit, however many stages a
+    warp's ring has (8 of 16 dims)."""
+    b = R.Batch([3000, 500], 2, dim, 16, seed=22)
+    q = queries(b, 8, 22)
+    with Cache(b, kv_type, cuda_device) as c:
+        c.append()
+        ws = torch.full((L.lora_attend_workspace_bytes(c.kv, 8),), 255, dtype=torch.uint8, device=cuda_device)
+        want, _ = attend(c, q, ws=ws)
+        qd = q.to(cuda_device)
+        out = torch.full_like(qd, 7.0)
+        limit = 0.1  # counted in cycles of a 2 GHz clock: up to 2 GHz / the SM's clock times as long
+        start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        L.lora_set_wait_limit_ns(int(limit * 1e9))
+        try:
+            start.record()
+            L.lora_selftest_stalled_attend(c.kv, 0, qd, out, c.table, c.lens, ws)
+            end.record()
+            torch.cuda.synchronize()
+        finally:
+            L.lora_set_wait_limit_ns(0)
+        assert 0.9 * limit <= start.elapsed_time(end) * 1e-3 <= 2.5 * limit
+        assert c.error() == L.LORA_ERR_TIMEOUT and (out == 7.0).all()
+        got, _ = attend(c, q, ws=ws)
+        assert torch.equal(got, want) and c.error() == L.LORA_OK
