@@ -38,8 +38,8 @@
 // A operand.  (With the heads as M half of each instruction and of the
 // accumulators would be padding; tcgen05 takes no fewer than 64 rows.)  The
 // weights leave S^T token by token and are needed head by head: one movmatrix
-// per 8 x 8 block turns them.  8-bit codes are multiplied as they are (int8 keys) or become
-// fp16 exactly, in 3 to 5 instructions per four; K's scales multiply the
+// per 8 x 8 block turns them.  8-bit codes become
+// fp16 exactly, in 2 to 5 instructions per four; K's scales multiply the
 // scores, V's the weights, in fp32.
 //
 // Tokens outside the range get weight 0 by selection, not by adding: what lies
@@ -131,13 +131,6 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ void mma_s8(int (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                       uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-      : "+r"(c[0]), "+r"(c[1]), "+r"(c[2]), "+r"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -172,24 +165,33 @@ __device__ __forceinline__ void key_codes_to_f16(uint32_t w, uint32_t &a, uint32
     codes_to_f16<TYPE>(w, a, b);
 }
 
-// How the scores of a unit are formed.
-//  kBf16: q as it is, times bf16 keys.
-//  kF16:  q scaled per head by a power of two to below 2, as fp16: exact down to
-//         2^-14 of the head's largest |q|, below that off by at most 2^-25 of it.
-//         Keys become fp16 exactly.  (The warp-level product of e4m3 operands is
-//         no single instruction of this GPU: it took 1.7 times the instructions
-//         of this form.)
-//  kInt8: q = (hi + lo / 128 + rest / 16384) * amax / 127, all int8: off by at most
-//         2^-22 of the largest |q|.  Keys are multiplied as the codes they are;
-//         products and sums are exact.  (Not for 9 to 16 heads wider than 128: the
-//         three terms would take more registers than there are.)
-enum { kBf16, kF16, kInt8 };
-__host__ __device__ constexpr int score_form(int type, int dim, int nt) {
-  return type == LORA_KV_BF16 ? kBf16 : type == LORA_KV_INT8 && (nt == 1 || dim <= 128) ? kInt8 : kF16;
+// The same word of K codes as two bf16 pairs, exactly: e4m3 codes times 2^-120 (their
+// bits in bf16's place: its exponents start that much lower); int8 as the
+// difference of 128 + the code's low bits and 128 or, where it is negative, 256.
+constexpr float kFineScale = 0x1p120f;
+template <int TYPE>
+__device__ __forceinline__ void key_codes_to_bf16(uint32_t w, uint32_t &a, uint32_t &b) {
+  if (TYPE == LORA_KV_E4M3) {
+    const uint32_t x = __byte_perm(w, 0, 0x1404), y = __byte_perm(w, 0, 0x3424);
+    a = (x & 0x80008000u) | (x >> 4 & 0x07f007f0u);
+    b = (y & 0x80008000u) | (y >> 4 & 0x07f007f0u);
+  } else {
+    const uint32_t x = __byte_perm(w, 0x43434343u, 0x4240), y = __byte_perm(w, 0x43434343u, 0x4341);
+    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(a) : "r"(x & 0xff7fff7fu), "r"(x & 0xff80ff80u));
+    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(b) : "r"(y & 0xff7fff7fu), "r"(y & 0xff80ff80u));
+  }
 }
-__host__ __device__ constexpr int q_regs(int form, int nb, int nt) {  // per n-tile: 6 for two blocks, or 2 a block
-  return nt * (form == kInt8 ? (nb + 1) / 2 * 6 : nb * 2);
-}
+
+// Over a bf16 cache scores are q as it is times the keys.  Over an 8-bit cache keys
+// become fp16 exactly, and q is scaled per head by a power of two to below 2^16: fp16
+// then has all bits of what is 2^-kFine of the head's largest |q| or more.  A unit with
+// a smaller q is multiplied in bf16 instead, which has all of q and of the codes too
+// but takes more instructions to make.  (As three int8 terms times int8 codes, 2^-22
+// of the largest |q| was lost and 256 requests of 2000 int8 tokens took 105.5 us
+// instead of 103.9; the warp-level product of e4m3 operands is no single instruction
+// of this GPU and took 1.7 times the instructions.)
+constexpr float kQTop = 0x1p15f;
+constexpr int kFine = 32;
 
 // A length that is attended to, else 0 (none, empty, in error).
 __device__ __forceinline__ int valid_len(const KvView &kv, const KvSeqs &s, int len) {
@@ -580,10 +582,9 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(KvView kv, KvSeqs
     const uint32_t v_row = (kTileTokens + (TYPE == LORA_KV_BF16 ? mat >> 1 : mat & 1) * 8 + r8) * row_bytes;
     const int k_c = mat >> 1, v_c = TYPE == LORA_KV_BF16 ? mat & 1 : mat >> 1;
 
-    constexpr int FORM = score_form(TYPE, DIM, NT);
-    constexpr int QN = q_regs(FORM, NB, 1);
-    uint32_t qa[NT][QN];
-    float qs[NT][2];  // what a score is multiplied by: the softmax's scale and that of q's terms
+    uint32_t qa[NT][2 * NB];
+    float qs[NT][2];  // what a score is multiplied by: the softmax's scale and q's
+    unsigned fine = 0;  // (8 bits) not 0: the unit's scores are formed in bf16; byte h: exponent of what row 8 h + g of q is divided by
     float o[NT][NB][4], m[NT][2], l[NT][2];
     float w[NT][2];  // (8 bits) reference of the weights times V's scales
     int cseq = -1, cunit = -1, cpos = 0, clen = 0, cfirst = 0;  // of the step to compute; cfirst: the unit's first token
@@ -594,64 +595,60 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(KvView kv, KvSeqs
     // q as the products' B operand: columns = heads, rows = dims in the order of the K operand
     auto load_q = [&]() {
       const int kvh = unit_kvh(cunit), h0 = unit_h0(cunit), j = lane & 3;
+      bool more = false;
+      unsigned exps = 0;
 #pragma unroll
       for (int h = 0; h < NT; ++h) {
         const bool live = h0 + g + 8 * h < a.group;
         const uint8_t *q = a.q + cseq * a.ldq + (long long)(kvh * a.group + h0 + g + 8 * h) * dim * 2;
-        uint2 u[NB];  // bf16: dims 16 b + 2 j, + 1, + 8, + 9; 8 bits: dims 16 b + 4 j ..
+        uint32_t(&u)[2 * NB] = qa[h];  // bf16: dims 16 b + 2 j, + 1, + 8, + 9; 8 bits: dims 16 b + 4 j ..
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
-          u[b] = make_uint2(0, 0);
+          u[2 * b] = u[2 * b + 1] = 0;
           if (!live || (ANY && b >= nb)) continue;
           if (TYPE == LORA_KV_BF16) {
-            u[b].x = __ldg(reinterpret_cast<const uint32_t *>(q + b * 32 + j * 4));
-            u[b].y = __ldg(reinterpret_cast<const uint32_t *>(q + b * 32 + j * 4 + 16));
+            u[2 * b] = __ldg(reinterpret_cast<const uint32_t *>(q + b * 32 + j * 4));
+            u[2 * b + 1] = __ldg(reinterpret_cast<const uint32_t *>(q + b * 32 + j * 4 + 16));
           } else {
-            u[b] = __ldg(reinterpret_cast<const uint2 *>(q + b * 32 + j * 8));
+            const uint2 x = __ldg(reinterpret_cast<const uint2 *>(q + b * 32 + j * 8));
+            u[2 * b] = x.x;
+            u[2 * b + 1] = x.y;
           }
         }
-        if (FORM == kBf16) {
+        if (TYPE == LORA_KV_BF16) {
           qs[h][0] = qs[h][1] = a.scale2;
-#pragma unroll
-          for (int b = 0; b < NB; ++b) {
-            qa[h][b * 2] = u[b].x;
-            qa[h][b * 2 + 1] = u[b].y;
-          }
           continue;
         }
-        uint32_t top = 0;  // bits of the head's largest |q|
+        uint32_t top = 0, low = ~0u;  // bits of the head's largest |q|, and of the least but 0 (less 1), two by two
 #pragma unroll
-        for (int b = 0; b < NB; ++b)
-          top = max(top, max(max(u[b].x & 0x7fffu, (u[b].x >> 16) & 0x7fffu), max(u[b].y & 0x7fffu, (u[b].y >> 16) & 0x7fffu)));
+        for (int i = 0; i < 2 * NB; ++i) {
+          top = __vmaxu2(top, u[i] & 0x7fff7fffu);
+          low = __vminu2(low, ((u[i] | 0x80008000u) - 0x00010001u) ^ 0x80008000u);
+        }
+        top = max(top & 0xffffu, top >> 16);
+        low = min(low & 0xffffu, low >> 16);
         top = max(top, __shfl_xor_sync(~0u, top, 1));
         top = max(top, __shfl_xor_sync(~0u, top, 2));
-        const float amax = fmaxf(__uint_as_float(top << 16), 0x1p-100f);  // (a NaN is lost here and comes back below)
+        more |= (int)low < (int)(top & 0x7f80u) - (kFine << 7);
+        const float amax = fmaxf(__uint_as_float(top << 16), 0x1p-111f);  // (a NaN is lost here and comes back below)
         const float two = __uint_as_float(__float_as_uint(amax) & 0x7f800000u);  // 2^E, 2^E <= amax
-        const float mul = FORM == kInt8 ? 127.f / amax : 1.f / two;
-        float mine = FORM == kInt8 ? amax * (1.f / (127.f * 16384.f)) : two;
-        mine = top >= 0x7f80u ? __int_as_float(0x7fc00000) : mine * a.scale2;
+        const float mul = __uint_as_float(__float_as_uint(kQTop) + __float_as_uint(1.f) - __float_as_uint(two));  // kQTop / two
+        exps |= __float_as_uint(two) >> 23 << (8 * h);
+        const float mine = top >= 0x7f80u ? __int_as_float(0x7fc00000) : two * (a.scale2 / kQTop);
         qs[h][0] = __shfl_sync(~0u, mine, 4 * j2);
         qs[h][1] = __shfl_sync(~0u, mine, 4 * j2 + 4);
 #pragma unroll
-        for (int b = 0; b < NB; ++b) {
-          float x[4] = {bf16_lo(u[b].x) * mul, bf16_hi(u[b].x) * mul, bf16_lo(u[b].y) * mul, bf16_hi(u[b].y) * mul};
-          if (FORM == kInt8) {
-#pragma unroll
-            for (int k = 0; k < 3; ++k) {  // adding 1.5 * 2^23 rounds to an integer, in the sum's low bits
-              float y[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e) y[e] = x[e] + 12582912.f;
-              const uint32_t lo = __byte_perm(__float_as_uint(y[0]), __float_as_uint(y[1]), 0x0040);
-              const uint32_t hi = __byte_perm(__float_as_uint(y[2]), __float_as_uint(y[3]), 0x0040);
-              qa[h][(b >> 1) * 6 + 2 * k + (b & 1)] = __byte_perm(lo, hi, 0x5410);
-#pragma unroll
-              for (int e = 0; e < 4; ++e) x[e] = (x[e] - (y[e] - 12582912.f)) * 128.f;
-            }
-          } else {  // as key_codes_to_f16 pairs the dims
-            qa[h][b * 2] = TYPE == LORA_KV_E4M3 ? pack_f16x2(x[0], x[1]) : pack_f16x2(x[0], x[2]);
-            qa[h][b * 2 + 1] = TYPE == LORA_KV_E4M3 ? pack_f16x2(x[2], x[3]) : pack_f16x2(x[1], x[3]);
-          }
+        for (int b = 0; b < NB; ++b) {  // as key_codes_to_f16 pairs the dims
+          const float x0 = bf16_lo(u[2 * b]) * mul, x1 = bf16_hi(u[2 * b]) * mul;
+          const float x2 = bf16_lo(u[2 * b + 1]) * mul, x3 = bf16_hi(u[2 * b + 1]) * mul;
+          u[2 * b] = TYPE == LORA_KV_E4M3 ? pack_f16x2(x0, x1) : pack_f16x2(x0, x2);
+          u[2 * b + 1] = TYPE == LORA_KV_E4M3 ? pack_f16x2(x2, x3) : pack_f16x2(x1, x3);
         }
+      }
+      fine = __any_sync(~0u, more) ? exps : 0;
+      if (fine) {
+#pragma unroll
+        for (int h = 0; h < NT; ++h) qs[h][0] *= kQTop, qs[h][1] *= kQTop;
       }
     };
 
@@ -821,10 +818,9 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(KvView kv, KvSeqs
       for (int t = 0; t < TT; ++t) {
         const uint32_t k32 = st32 + t * tile_bytes + k_row;
         float d[NT][4] = {};  // a second sum for the odd blocks: a shorter chain
-        int ci[3][NT][4] = {};
 #pragma unroll
         for (int h = 0; h < NT; ++h) c[t][h][0] = c[t][h][1] = c[t][h][2] = c[t][h][3] = 0.f;
-        if (FORM == kBf16) {
+        if (TYPE == LORA_KV_BF16) {
 #pragma unroll
           for (int b = 0; b < NB; ++b) {
             if (ANY && b >= nb) continue;
@@ -835,18 +831,12 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(KvView kv, KvSeqs
               mma16816(b & 1 ? d[h] : c[t][h], k[0], k[1], k[2], k[3], qa[h][2 * b], qa[h][2 * b + 1]);
           }
         } else {
+          if (!fine) {
 #pragma unroll
-          for (int p = 0; p < (NB + 1) / 2; ++p) {
-            if (ANY && 2 * p >= nb) continue;
-            uint32_t w[4];  // (tokens 0-7 | 8-15) x (block 2p | 2p + 1)
-            ldsm4(w, k32 + (((2 * p + k_c) ^ sw) << 4));
-            if (FORM == kInt8) {  // (past the row's end q's terms are 0 and any code will do)
-#pragma unroll
-              for (int h = 0; h < NT; ++h)
-#pragma unroll
-                for (int k = 0; k < 3; ++k)
-                  mma_s8(ci[k][h], w[0], w[1], w[2], w[3], qa[h][p * 6 + 2 * k], qa[h][p * 6 + 2 * k + 1]);
-            } else {
+            for (int p = 0; p < (NB + 1) / 2; ++p) {
+              if (ANY && 2 * p >= nb) continue;
+              uint32_t w[4];  // (tokens 0-7 | 8-15) x (block 2p | 2p + 1)
+              ldsm4(w, k32 + (((2 * p + k_c) ^ sw) << 4));
 #pragma unroll
               for (int x = 0; x < 2; ++x) {
                 const int b = 2 * p + x;
@@ -856,6 +846,26 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(KvView kv, KvSeqs
                 key_codes_to_f16<TYPE>(w[2 * x + 1], k1, k3);
 #pragma unroll
                 for (int h = 0; h < NT; ++h) mma_f16(x ? d[h] : c[t][h], k0, k1, k2, k3, qa[h][2 * b], qa[h][2 * b + 1]);
+              }
+            }
+          } else {  // (rare: q is read again, and nothing of it kept in registers)
+            const uint8_t *q = a.q + cseq * a.ldq + ((long long)(unit_kvh(cunit) * a.group + unit_h0(cunit)) * dim + 4 * (lane & 3)) * 2;
+#pragma unroll 1
+            for (int b = 0; b < nb; ++b) {
+              uint32_t w[4], k0, k1, k2, k3;
+              ldsm4(w, k32 + ((((b & ~1) + k_c) ^ sw) << 4));
+              key_codes_to_bf16<TYPE>(b & 1 ? w[2] : w[0], k0, k2);
+              key_codes_to_bf16<TYPE>(b & 1 ? w[3] : w[1], k1, k3);
+#pragma unroll
+              for (int h = 0; h < NT; ++h) {
+                const float one = 1.f / __uint_as_float((fine >> (8 * h) & 255u) << 23), up = TYPE == LORA_KV_E4M3 ? kFineScale : 1.f;
+                uint2 u = make_uint2(0, 0);
+                if (unit_h0(cunit) + g + 8 * h < a.group)
+                  u = __ldg(reinterpret_cast<const uint2 *>(q + ((g + 8 * h) * dim + b * 16) * 2));
+                const float x0 = bf16_lo(u.x) * one * up, x1 = bf16_hi(u.x) * one * up;
+                const float x2 = bf16_lo(u.y) * one * up, x3 = bf16_hi(u.y) * one * up;
+                mma16816(d[h], k0, k1, k2, k3, TYPE == LORA_KV_E4M3 ? pack_bf16x2(x0, x1) : pack_bf16x2(x0, x2),
+                         TYPE == LORA_KV_E4M3 ? pack_bf16x2(x2, x3) : pack_bf16x2(x1, x3));
               }
             }
           }
@@ -870,10 +880,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(KvView kv, KvSeqs
         for (int h = 0; h < NT; ++h)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            if (FORM == kInt8)
-              c[t][h][e] = fmaf((float)(ci[0][h][e] * 128 + ci[1][h][e]), 128.f, (float)ci[2][h][e]);
-            else
-              c[t][h][e] += d[h][e];
+            c[t][h][e] += d[h][e];
             c[t][h][e] *= TYPE == LORA_KV_BF16 ? qs[h][e & 1] : ks[e >> 1] * qs[h][e & 1];
           }
       }

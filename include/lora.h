@@ -640,7 +640,8 @@ LORA_API size_t lora_attend_workspace_bytes(const lora_kv *kv, int n_heads);
  *   ws, ws_bytes device workspace of lora_attend_workspace_bytes, 16-byte
  *                aligned; its content need not survive between calls, and calls
  *                that may overlap on the GPU need one each
- * Scores, statistics and sums are fp32; out is rounded once.  The weights that
+ * Scores, statistics and sums are fp32; out is rounded once.  q enters the products
+ * with all its bits (over an 8-bit cache those above 2^-120 of its head's largest).  The weights that
  * multiply V are rounded: over a bf16 cache to 16 bits; over an 8-bit cache,
  * times V's scale, to fp16 (2^-11 of itself, or 2^-36 of the head's largest such
  * product).  A sequence of length

@@ -129,3 +129,52 @@ def test_small_and_no_values(cuda_device, kv_type):
         c.append()
         out, lse = attend(c, q)
         assert (out == 0).all() and torch.isfinite(lse).all()
+
+
+@pytest.mark.parametrize("kv_type", list(R.TYPES))
+@pytest.mark.parametrize("spread", [5, 10, 14, 17, 18, 20, 24, 30, 60])
+@pytest.mark.parametrize("heads,kv_heads,dim", [(8, 2, 64), (4, 4, 128), (16, 1, 256), (20, 2, 48), (3, 1, 16), (12, 1, 176)])
+def test_large_queries_where_keys_are_zero(cuda_device, kv_type, spread, heads, kv_heads, dim):
+    """Some dims of q are 2^spread times the others, and the keys have nothing there: the scores come from the others."""
+    b = R.Batch([300, 1, 5000, 64], kv_heads, dim, 16, seed=34)
+    q = queries(b, heads, 34, gain=3.0)
+    wide = [0, 5] if spread % 2 else [dim - 1]
+    g = q.view(len(b.lens), heads, dim)
+    g[..., wide] *= 2.0 ** spread
+    g[2, :, 1] = 0
+    for k in b.k:
+        k[..., wide] = 0
+    with Cache(b, kv_type, cuda_device) as c:
+        c.append()
+        hold(b, kv_type, q, attend(c, q)[0])
+        small = (q.float() * 2.0 ** -80).to(torch.bfloat16)  # (and far from 1: the scale brings it back)
+        for i, n in enumerate(b.lens):
+            assert torch.equal(small[i].double() * 2.0 ** 80, q[i].double())
+        out = attend(c, small, scale=dim ** -0.5 * 2.0 ** 80)[0]
+        hold(b, kv_type, q, out)
+
+
+@pytest.mark.parametrize("kv_type", ["e4m3", "int8"])
+@pytest.mark.parametrize("spread", [3, 25])
+def test_every_code_of_a_key(cuda_device, kv_type, spread):
+    """Keys of all codes, the lowest of a row's range among them, whose largest meets a q of 0."""
+    dim = 128
+    b = R.Batch([256, 40], 1, dim, 16, seed=35)
+    codes = torch.arange(1, 128).double()
+    if kv_type == "e4m3":
+        codes = torch.arange(1, 127, dtype=torch.uint8).view(torch.float8_e4m3fn).double()  # 2^-9 to 448
+    g = torch.Generator().manual_seed(35)
+    for k in b.k:
+        pick = codes[torch.randint(len(codes), k.shape, generator=g)]
+        pick[::2] = codes[torch.randint(7, pick[::2].shape, generator=g)]
+        pick = pick * (torch.randint(2, k.shape, generator=g) * 2 - 1)
+        pick[..., 9] = R.QMAX[kv_type]
+        pick[..., 3] = 0
+        k.copy_((pick / 16).to(torch.bfloat16))
+    q = queries(b, 4, 35, gain=0.5)
+    v = q.view(2, 4, dim)
+    v[..., 9] = 0
+    v[..., 3] *= 2.0 ** spread
+    with Cache(b, kv_type, cuda_device) as c:
+        c.append()
+        hold(b, kv_type, q, attend(c, q)[0])
