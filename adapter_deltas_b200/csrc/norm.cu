@@ -84,14 +84,40 @@ __global__ void __launch_bounds__(kNormMaxThreads) rmsnorm_kernel(NormArgs a) {
     }
   }
   const int width = min(a.tpr, 32);
-  for (int d = width / 2; d; d >>= 1) ss += __shfl_xor_sync(~0u, ss, d);
-  if (nw > 1) {
-    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = ss;
-    __syncthreads();
+  auto row_sum = [&](float x) {
+    for (int d = width / 2; d; d >>= 1) x += __shfl_xor_sync(~0u, x, d);
+    if (nw > 1) {
+      if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = x;
+      __syncthreads();
+      x = 0.f;
+      for (int i = 0; i < nw; ++i) x += part[slot * nw + i];
+    }
+    return x;
+  };
+  ss = row_sum(ss);
+  const float mean = ss / a.d + a.eps;
+  float inv = __fdiv_rn(1.f, __fsqrt_rn(mean));
+  // Squares past fp32's range (h from 2^56 on), or too small for its bits with no eps
+  // above them: once more in units that bring them back (all warps of a row agree).
+  // Small h are brought to their unit before the product too, since 1 / rms may pass
+  // the range; large ones are not, since a row's smallest would lose bits.
+  bool small = false;
+  const bool far = !(mean >= 0x1p-100f && mean < INFINITY);
+  if (__builtin_expect(__any_sync(~0u, far), 0)) {
+    small = mean < 0x1p-100f;
+    const float unit = small ? 0x1p80f : far ? 0x1p-80f : 1.f;
     ss = 0.f;
-    for (int i = 0; i < nw; ++i) ss += part[slot * nw + i];
+#pragma unroll
+    for (int i = 0; i < VPT; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float t = h[i][e] * unit;
+        ss = fmaf(t, t, ss);
+      }
+    if (nw > 1) __syncthreads();  // (part has been read)
+    ss = row_sum(ss);
+    inv = __fdiv_rn(1.f, __fsqrt_rn(ss / a.d + a.eps * unit * unit)) * fminf(unit, 1.f);
   }
-  const float inv = __fdiv_rn(1.f, __fsqrt_rn(ss / a.d + a.eps));
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
     const int v = lane + i * a.tpr;
@@ -99,6 +125,10 @@ __global__ void __launch_bounds__(kNormMaxThreads) rmsnorm_kernel(NormArgs a) {
       *reinterpret_cast<uint4 *>(sum + i * hop) =
           make_uint4(pack_bf16x2(h[i][0], h[i][1]), pack_bf16x2(h[i][2], h[i][3]), pack_bf16x2(h[i][4], h[i][5]),
                      pack_bf16x2(h[i][6], h[i][7]));
+    if (__builtin_expect(small, 0)) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) h[i][e] *= 0x1p80f;
+    }
     float g[8];
     unpack8(w[i], g);
 #pragma unroll
