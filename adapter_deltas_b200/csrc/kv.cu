@@ -316,6 +316,10 @@ __global__ void __launch_bounds__(kRowThreads, kRowBlocks) kv_gather_kernel(KvVi
   }
 }
 
+// Reads and clears the status in one access: what another stream's call reports in
+// between is in this reading or the next.
+__global__ void kv_take_status_kernel(int *status, int *out) { *out = atomicExch(status, 0); }
+
 }  // namespace lora
 
 using namespace lora;
@@ -455,8 +459,14 @@ int lora_kv_create(lora_kv **out, int device, int n_layers, int n_pages, int pag
   kv->mem = static_cast<uint8_t *>(kv_mem);
   DeviceGuard g(device);
   int rc = cuda_status(cudaDeviceGetAttribute(&kv->n_sm, cudaDevAttrMultiProcessorCount, device));
-  if (rc == LORA_OK) rc = cuda_status(cudaMalloc(&kv->d_status, 256));
-  if (rc == LORA_OK) rc = cuda_status(cudaMemset(kv->d_status, 0, 256));
+  if (rc == LORA_OK) rc = cuda_status(cudaMalloc(&kv->d_status, kKvStatusInts * sizeof(int)));
+  if (rc == LORA_OK) {  // (on a stream that waits for no other: done before the first call on any)
+    cudaStream_t st = nullptr;
+    rc = cuda_status(cudaStreamCreateWithFlags(&st, cudaStreamNonBlocking));
+    if (rc == LORA_OK) rc = cuda_status(cudaMemsetAsync(kv->d_status, 0, kKvStatusInts * sizeof(int), st));
+    if (rc == LORA_OK) rc = cuda_status(cudaStreamSynchronize(st));
+    if (st) (void)cudaStreamDestroy(st);
+  }
   if (rc == LORA_OK) rc = attend_setup(kv);
   if (rc != LORA_OK) {
     if (kv->d_status) (void)cudaFree(kv->d_status);
@@ -483,10 +493,17 @@ int lora_kv_destroy(lora_kv *kv) {
 int lora_kv_get_error(lora_kv *kv, int *device_status, void *stream) {
   if (!kv || !device_status) return LORA_ERR_INVALID_ARG;
   DeviceGuard g(kv->device);
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
   int v = 0;
-  int rc = cuda_status(cudaStreamSynchronize(static_cast<cudaStream_t>(stream)));
-  if (rc == LORA_OK) rc = cuda_status(cudaMemcpy(&v, kv->d_status, 4, cudaMemcpyDeviceToHost));
-  if (rc == LORA_OK) rc = cuda_status(cudaMemset(kv->d_status, 0, 4));
+  int rc = cuda_status(cudaStreamSynchronize(st));  // (also refuses a stream that is being captured)
+  if (rc == LORA_OK) {
+    int *out = kv->d_status + 1 + kv->takes.fetch_add(1) % (kKvStatusInts - 1);
+    kv_take_status_kernel<<<1, 1, 0, st>>>(kv->d_status, out);
+    rc = cuda_status(cudaGetLastError());
+    if (rc == LORA_OK) g_launches.fetch_add(1);
+    if (rc == LORA_OK) rc = cuda_status(cudaMemcpyAsync(&v, out, 4, cudaMemcpyDeviceToHost, st));
+    if (rc == LORA_OK) rc = cuda_status(cudaStreamSynchronize(st));
+  }
   if (rc == LORA_OK) *device_status = v;
   return rc;
 }

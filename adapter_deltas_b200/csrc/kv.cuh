@@ -10,6 +10,8 @@
 // fall into different shared-memory banks with no padding and no staging pass.
 #pragma once
 
+#include <atomic>
+
 #include "internal.cuh"
 
 namespace lora {
@@ -20,6 +22,7 @@ constexpr int kKvMaxHeads = 1024;   // key heads
 constexpr int kKvMaxQHeads = 4096;  // query heads
 constexpr int kKvMaxLayers = 4096;
 constexpr int kKvMaxPageTokens = 1024;
+constexpr int kKvStatusInts = 64;
 
 __host__ __device__ constexpr int kv_elt(int type) { return type == LORA_KV_BF16 ? 2 : 1; }
 __host__ __device__ constexpr int kv_row_bytes(int type, int dim) { return dim * kv_elt(type); }
@@ -194,7 +197,8 @@ struct lora_kv {
   int n_layers = 0, n_pages = 0, page_tokens = 0, log2_page = 0, heads = 0, dim = 0, type = 0;
   long long page_bytes = 0, layer_bytes = 0;
   uint8_t *mem = nullptr;
-  int *d_status = nullptr;
+  int *d_status = nullptr;  // [kKvStatusInts]: the status, then places for readings of it
+  std::atomic<unsigned> takes{0};
   int n_sm = 0;
 
   lora::KvView view(int layer) const {

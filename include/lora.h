@@ -579,7 +579,9 @@ LORA_API int lora_kv_create(lora_kv **out, int device, int n_layers, int n_pages
 /* Synchronise the device and free the handle (kv_mem stays the caller's). */
 LORA_API int lora_kv_destroy(lora_kv *kv);
 
-/* As lora_get_error, for a cache's calls. */
+/* As lora_get_error, for a cache's calls.  Waits for `stream` alone; reading and
+ * clearing are one step, so that what calls on other streams report meanwhile
+ * is not lost. */
 LORA_API int lora_kv_get_error(lora_kv *kv, int *device_status, void *stream);
 
 /*
