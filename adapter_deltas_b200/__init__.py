@@ -392,6 +392,12 @@ class KvHandle:
 # microseconds on the GPU: their checks read each property of a tensor once.
 
 
+def _refuse_past_int(bits: int, where: str) -> None:
+    """bits: sizes and indices or'ed together; one past a C int (which ctypes would cut) or below 0 is refused."""
+    if bits >> 31:
+        _check(LORA_ERR_INVALID_ARG, where)
+
+
 def _rows(t, name: str, device: int, shape, dtype, where: str):
     """Address and leading dimension of a [T, ld] operand whose rows of shape[1] values are reached by its row stride."""
     if t.shape == shape and t.is_contiguous() and t.dtype is dtype and t.get_device() == device:
@@ -399,7 +405,9 @@ def _rows(t, name: str, device: int, shape, dtype, where: str):
     if t.dtype is not dtype or t.get_device() != device or t.shape != shape or (t.stride(1) != 1 and shape[1] > 1):
         raise ValueError("%s: %s must be %s %s with unit column stride on cuda:%d, not %s %s %s"
                          % (where, name, dtype, list(shape), device, t.dtype, tuple(t.shape), t.device))
-    return t.data_ptr(), t.stride(0) if shape[0] > 1 else (shape[1] + 7) // 8 * 8
+    ld = t.stride(0) if shape[0] > 1 else (shape[1] + 7) // 8 * 8
+    _refuse_past_int(ld, where)
+    return t.data_ptr(), ld
 
 
 def _dense(t, name: str, device: int, shape, dtype, where: str) -> int:
@@ -419,6 +427,8 @@ def _stream_on(stream, device: int) -> int:
 
 def lora_kv_bytes_required(n_layers: int, n_pages: int, page_tokens: int, n_kv_heads: int, head_dim: int,
                            kv_type: int) -> int:
+    if (n_layers | n_pages | page_tokens | n_kv_heads | head_dim | kv_type) >> 31:
+        return 0
     return int(_lib.lora_kv_bytes_required(n_layers, n_pages, page_tokens, n_kv_heads, head_dim, kv_type))
 
 
@@ -427,6 +437,7 @@ def lora_kv_create(device: int, n_layers: int, n_pages: int, page_tokens: int, n
     """A paged key/value cache over the device tensor `kv_mem`."""
     if kv_mem.get_device() != device or not kv_mem.is_contiguous():
         raise ValueError("lora_kv_create: kv_mem must be contiguous on cuda:%d" % device)
+    _refuse_past_int(n_layers | n_pages | page_tokens | n_kv_heads | head_dim | kv_type, "lora_kv_create")
     out = _P()
     _check(_lib.lora_kv_create(ctypes.byref(out), device, n_layers, n_pages, page_tokens, n_kv_heads, head_dim, kv_type,
                                kv_mem.data_ptr(), kv_mem.numel() * kv_mem.element_size()), "lora_kv_create")
@@ -450,6 +461,7 @@ def _kv_rows(fn, where: str, kv: KvHandle, layer: int, k, v, page_table, seq_len
     dev, T, n, paged = kv.device, k.shape[0], seq_lens.shape[0], page_table.shape
     if len(paged) != 2:
         raise ValueError("%s: page_table must be [n_seqs, max_pages]" % where)
+    _refuse_past_int(layer | T | n | paged[1], where)
     shape = (T, kv.n_kv_heads * kv.head_dim)
     kp, ldk = _rows(k, "k", dev, shape, torch.bfloat16, where)
     vp, ldv = _rows(v, "v", dev, shape, torch.bfloat16, where)
@@ -472,18 +484,20 @@ def lora_kv_gather(kv: KvHandle, layer: int, k, v, page_table, seq_lens, row_off
 
 
 def lora_attend_workspace_bytes(kv: KvHandle, n_heads: int) -> int:
-    return int(_lib.lora_attend_workspace_bytes(kv, n_heads))
+    return 0 if n_heads >> 31 else int(_lib.lora_attend_workspace_bytes(kv, n_heads))
 
 
 def lora_attend(kv: KvHandle, layer: int, q, out, page_table, seq_lens, ws, scale: Optional[float] = None,
                 window: int = 0, sinks=None, lse=None, stream=None) -> None:
     """Attention of one new token per sequence over the cache: q, out bf16 [n_seqs, n_heads * head_dim]; scale
-    1 / sqrt(head_dim) by default; sinks fp32 [n_heads] or None; lse fp32 [n_seqs, n_heads] or None."""
+    1 / sqrt(head_dim) by default; sinks fp32 [n_heads] or None; lse fp32 [n_seqs, n_heads] or None.  A window past
+    2^30 is all of any sequence."""
     import torch
     dev, n, width, paged = kv.device, seq_lens.shape[0], q.shape[-1], page_table.shape
     where, n_heads = "lora_attend", width // kv.head_dim
     if width % kv.head_dim or len(paged) != 2:
         raise ValueError("%s: q must be [n_seqs, n_heads * head_dim], page_table [n_seqs, max_pages]" % where)
+    _refuse_past_int(layer | n | paged[1] | n_heads | (-1 if window < 0 else 0), where)
     shape = (n, width)
     qp, ldq = _rows(q, "q", dev, shape, torch.bfloat16, where)
     op, ldo = _rows(out, "out", dev, shape, torch.bfloat16, where)
@@ -494,8 +508,8 @@ def lora_attend(kv: KvHandle, layer: int, q, out, page_table, seq_lens, ws, scal
     ws_bytes = ws.numel()
     wp = _dense(ws, "ws", dev, (ws_bytes,), torch.uint8, where)
     _check(_lib.lora_attend(kv, layer, qp, ldq, op, ldo, lp, sp, n_heads, table, paged[1], lens, n,
-                            kv.head_dim ** -0.5 if scale is None else scale, window, wp, ws_bytes,
-                            _stream_on(stream, dev)), where)
+                            kv.head_dim ** -0.5 if scale is None else scale, min(window, 1 << 30), wp,
+                            ws_bytes, _stream_on(stream, dev)), where)
 
 
 def lora_rmsnorm(x, weight, eps: float, residual=None, residual_out=None, y=None, q=None, q_scales=None,
@@ -505,6 +519,7 @@ def lora_rmsnorm(x, weight, eps: float, residual=None, residual_out=None, y=None
     import torch
     where, dev, shape, bf16 = "lora_rmsnorm", x.get_device(), x.shape, torch.bfloat16
     T, d = shape
+    _refuse_past_int(T | d, where)
     xp, ldx = _rows(x, "x", dev, shape, bf16, where)
     wp = _dense(weight, "weight", dev, (d,), bf16, where)
     rp = op = yp = qp = None
