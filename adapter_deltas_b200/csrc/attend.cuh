@@ -586,7 +586,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(KvView kv, KvSeqs
     float qs[NT][2];  // what a score is multiplied by: the softmax's scale and q's
     unsigned fine = 0;  // (8 bits) not 0: the unit's scores are formed in bf16; byte h: exponent of what row 8 h + g of q is divided by
     float o[NT][NB][4], m[NT][2], l[NT][2];
-    float w[NT][2];  // (8 bits) reference of the weights times V's scales
+    float w[NT][2];  // (8 bits) reference of the weights times V's scales, from m
     int cseq = -1, cunit = -1, cpos = 0, clen = 0, cfirst = 0;  // of the step to compute; cfirst: the unit's first token
     bool cut_before = false, cnew = true;
     int stage = 0, fstage = 0;
@@ -679,7 +679,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(KvView kv, KvSeqs
           }
 #pragma unroll
           for (int h = 0; h < NT; ++h) {
-            float mul[2], half[2];  // (8 bits: 2^(w - m), which may pass the exponent's range, in two halves)
+            float mul[2], half[2];  // (8 bits: 2^w, which may pass the exponent's range, in two halves)
             bool on[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
@@ -688,7 +688,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(KvView kv, KvSeqs
               l[h][e] += __shfl_xor_sync(~0u, l[h][e], 16);
               const int r = 8 * h + j2 + e, hd = kvh * a.group + h0 + r;
               on[e] = r < a.rows && h0 + r < a.group;
-              half[e] = TYPE == LORA_KV_BF16 ? 1.f : w[h][e] == -INFINITY ? 0.f : exp2_fast(0.5f * (w[h][e] - m[h][e]));
+              half[e] = TYPE == LORA_KV_BF16 ? 1.f : exp2_fast(0.5f * w[h][e]);
               mul[e] = half[e];
               if (!on[e]) continue;
               if (whole) {
@@ -910,26 +910,33 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(KvView kv, KvSeqs
       }
       // m is a reference, within 2^kSlack of the running maximum: while no
       // score passes it by more, nothing is exchanged and nothing rescaled.  The
-      // values' sums have one of their own: with 8 bits w, by the weights times V's
+      // values' sums have one of their own: with 8 bits m + w, by the weights times V's
       // scales (in logarithms: their product may pass the exponent's range), which
       // leaves the largest of those between 2^kWeight and 2^(kWeight + kSlack).
       // (By V's largest scale alone a token with a far larger V and next to no
-      // weight would take the others' bits.)
+      // weight would take the others' bits.)  Logarithms are added to scores less m:
+      // a large score itself has no bits left for them.
       float mx[NT][2], wx[NT][2];
       bool moved = false;
+      auto finite = [](float x) { return x == -INFINITY ? 0.f : x; };
+      auto weighted_max = [&](int h, int e, float base) {
+        float x = -INFINITY;
+#pragma unroll
+        for (int t = 0; t < TT; ++t) x = fmaxf(x, fmaxf(c[t][h][e] - base + lv[t][0], c[t][h][e + 2] - base + lv[t][1]));
+        return x;
+      };
 #pragma unroll
       for (int h = 0; h < NT; ++h)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           mx[h][e] = c[0][h][e];
-          wx[h][e] = -INFINITY;
 #pragma unroll
-          for (int t = 0; t < TT; ++t) {
-            mx[h][e] = fmaxf(mx[h][e], fmaxf(c[t][h][e], c[t][h][e + 2]));
-            if (TYPE != LORA_KV_BF16) wx[h][e] = fmaxf(wx[h][e], fmaxf(c[t][h][e] + lv[t][0], c[t][h][e + 2] + lv[t][1]));
-          }
+          for (int t = 0; t < TT; ++t) mx[h][e] = fmaxf(mx[h][e], fmaxf(c[t][h][e], c[t][h][e + 2]));
           moved |= mx[h][e] > m[h][e] + kSlack;
-          if (TYPE != LORA_KV_BF16) moved |= wx[h][e] > w[h][e] + (kWeight + kSlack);
+          if (TYPE != LORA_KV_BF16) {
+            wx[h][e] = weighted_max(h, e, finite(m[h][e]));
+            moved |= wx[h][e] > w[h][e] + (kWeight + kSlack);
+          }
         }
       if (__any_sync(~0u, moved)) {
 #pragma unroll
@@ -941,15 +948,15 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(KvView kv, KvSeqs
               x = fmaxf(x, __shfl_xor_sync(~0u, x, 8));
               return fmaxf(x, __shfl_xor_sync(~0u, x, 16));
             };
-            auto raise = [](float &to, float x) {  // returns what was summed by the old one is worth
-              x = fmaxf(x, to);
-              const float alpha = exp2_fast(to - (x == -INFINITY ? 0.f : x));
-              to = x;
-              return alpha;
-            };
-            float alpha = raise(m[h][e], highest(mx[h][e]));
+            const float top = fmaxf(highest(mx[h][e]), m[h][e]), by = m[h][e] - finite(top);
+            m[h][e] = top;
+            float alpha = exp2_fast(by);
             l[h][e] *= alpha;
-            if (TYPE != LORA_KV_BF16) alpha = raise(w[h][e], highest(wx[h][e]) - kWeight);
+            if (TYPE != LORA_KV_BF16) {
+              const float was = w[h][e] + by;
+              w[h][e] = fmaxf(highest(weighted_max(h, e, finite(top))) - kWeight, was);
+              alpha = exp2_fast(was - finite(w[h][e]));
+            }
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
               if (ANY && b >= nb) continue;
@@ -968,13 +975,13 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(KvView kv, KvSeqs
       uint32_t pw[TERMS][TT][NT][2];
 #pragma unroll
       for (int h = 0; h < NT; ++h) {
-        const float base[2] = {m[h][0] == -INFINITY ? 0.f : m[h][0], m[h][1] == -INFINITY ? 0.f : m[h][1]};
-        const float wbase[2] = {w[h][0] == -INFINITY ? 0.f : w[h][0], w[h][1] == -INFINITY ? 0.f : w[h][1]};
+        const float base[2] = {finite(m[h][0]), finite(m[h][1])}, wbase[2] = {finite(w[h][0]), finite(w[h][1])};
 #pragma unroll
         for (int t = 0; t < TT; ++t)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {  // tokens g and g + 8
-            float p0 = exp2_fast(c[t][h][2 * e] - base[0]), p1 = exp2_fast(c[t][h][2 * e + 1] - base[1]);
+            const float x0 = c[t][h][2 * e] - base[0], x1 = c[t][h][2 * e + 1] - base[1];
+            const float p0 = exp2_fast(x0), p1 = exp2_fast(x1);
             l[h][0] += p0;
             l[h][1] += p1;
             if (TYPE == LORA_KV_BF16) {
@@ -982,8 +989,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(KvView kv, KvSeqs
               pw[0][t][h][e] = turn(hi2);
               pw[TERMS - 1][t][h][e] = turn(pack_bf16x2(p0 - bf16_lo(hi2), p1 - bf16_hi(hi2)));
             } else {
-              pw[0][t][h][e] = turn(pack_f16x2(exp2_fast(c[t][h][2 * e] + lv[t][e] - wbase[0]),
-                                               exp2_fast(c[t][h][2 * e + 1] + lv[t][e] - wbase[1])));
+              pw[0][t][h][e] = turn(pack_f16x2(exp2_fast(x0 + lv[t][e] - wbase[0]), exp2_fast(x1 + lv[t][e] - wbase[1])));
             }
           }
       }

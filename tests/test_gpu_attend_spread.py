@@ -178,3 +178,32 @@ def test_every_code_of_a_key(cuda_device, kv_type, spread):
     with Cache(b, kv_type, cuda_device) as c:
         c.append()
         hold(b, kv_type, q, attend(c, q)[0])
+
+
+@pytest.mark.parametrize("kv_type", list(R.TYPES))
+@pytest.mark.parametrize("size", [1, 10, 14, 20, 30, 60, 100])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_one_token_takes_all_whatever_its_score(cuda_device, kv_type, size, sign):
+    """Scores of 2^size and far apart: the result is the top token's value, which no error of a score touches: rounded
+    to bf16, its weight to fp16 over an 8-bit cache (2^-11), and 2^-15 for exponential and logarithm."""
+    heads, dim, top = 8, 64, [0, 100, 4999, 7]
+    b = R.Batch([1, 300, 5000, 40], 2, dim, 16, seed=36)
+    q = torch.zeros(4, heads, dim)
+    q[..., 5] = 2.0 ** (size / 2)
+    q[..., 9] = 2.0 ** (size / 2 - 20)
+    q = q.view(4, -1).to(torch.bfloat16)
+    for i, (k, v) in enumerate(zip(b.k, b.v)):
+        k.zero_()
+        k[..., 5] = sign * 2.0 ** (size / 2) * (0.25 if sign > 0 else 4.0)
+        k[top[i], :, 5] = sign * 2.0 ** (size / 2)
+        v[::3] *= 2.0 ** -30
+        v[1::3] *= 2.0 ** 30
+    scale = 200.0 if size < 10 else 1.0
+    with Cache(b, kv_type, cuda_device) as c:
+        c.append()
+        out, lse = attend(c, q, scale=scale)
+        for i, n in enumerate(b.lens):
+            want = R.values(b.v[i][top[i]], kv_type).repeat_interleave(heads // 2, 0)
+            got = out[i].view(heads, dim).double()
+            assert ((got - want).abs() <= want.abs() * (R.U_BF16 + 2.0 ** -11 + 2.0 ** -15)).all(), "sequence %d" % i
+        assert c.error() == 0
