@@ -219,7 +219,7 @@ __device__ __forceinline__ Ends finish(const float *sinks, int head, float m, fl
   base = base == -INFINITY ? 0.f : base;
   if (sinks) l = l * exp2_fast(m - base) + exp2_fast(sink - base);
   e.mul = l == 0.f ? 0.f : __fdividef(exp2_fast(m - base), l);  // (nothing has any weight: zeros, as without a token)
-  e.lse = fmaf(base, 0.693147181f, 0.693147181f * __log2f(l));
+  e.lse = (base + __log2f(l)) * 0.693147181f;
   return e;
 }
 
@@ -908,15 +908,16 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(KvView kv, KvSeqs
             }
           }
       }
-      // m is a reference, within 2^kSlack of the running maximum: while no
-      // score passes it by more, nothing is exchanged and nothing rescaled.  The
+      // m is a reference, up to kSlack above the running maximum: while no score
+      // passes it, nothing is exchanged and nothing rescaled, and no weight is above 1
+      // (V may be as large as its type allows).  The
       // values' sums have one of their own: with 8 bits m + w, by the weights times V's
       // scales (in logarithms: their product may pass the exponent's range), which
       // leaves the largest of those between 2^kWeight and 2^(kWeight + kSlack).
       // (By V's largest scale alone a token with a far larger V and next to no
       // weight would take the others' bits.)  Logarithms are added to scores less m:
       // a large score itself has no bits left for them.
-      float mx[NT][2], wx[NT][2];
+      float mx[NT][2];
       bool moved = false;
       auto finite = [](float x) { return x == -INFINITY ? 0.f : x; };
       auto weighted_max = [&](int h, int e, float base) {
@@ -932,11 +933,8 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(KvView kv, KvSeqs
           mx[h][e] = c[0][h][e];
 #pragma unroll
           for (int t = 0; t < TT; ++t) mx[h][e] = fmaxf(mx[h][e], fmaxf(c[t][h][e], c[t][h][e + 2]));
-          moved |= mx[h][e] > m[h][e] + kSlack;
-          if (TYPE != LORA_KV_BF16) {
-            wx[h][e] = weighted_max(h, e, finite(m[h][e]));
-            moved |= wx[h][e] > w[h][e] + (kWeight + kSlack);
-          }
+          moved |= mx[h][e] > m[h][e];
+          if (TYPE != LORA_KV_BF16) moved |= weighted_max(h, e, finite(m[h][e])) > w[h][e] + (kWeight + kSlack);
         }
       if (__any_sync(~0u, moved)) {
 #pragma unroll
@@ -948,7 +946,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(KvView kv, KvSeqs
               x = fmaxf(x, __shfl_xor_sync(~0u, x, 8));
               return fmaxf(x, __shfl_xor_sync(~0u, x, 16));
             };
-            const float top = fmaxf(highest(mx[h][e]), m[h][e]), by = m[h][e] - finite(top);
+            const float top = fmaxf(highest(mx[h][e]) + kSlack, m[h][e]), by = m[h][e] - finite(top);
             m[h][e] = top;
             float alpha = exp2_fast(by);
             l[h][e] *= alpha;

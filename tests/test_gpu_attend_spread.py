@@ -207,3 +207,27 @@ def test_one_token_takes_all_whatever_its_score(cuda_device, kv_type, size, sign
             got = out[i].view(heads, dim).double()
             assert ((got - want).abs() <= want.abs() * (R.U_BF16 + 2.0 ** -11 + 2.0 ** -15)).all(), "sequence %d" % i
         assert c.error() == 0
+
+
+@pytest.mark.parametrize("kv_type", list(R.TYPES))
+def test_values_near_the_end_of_the_range(cuda_device, kv_type):
+    """One token has V of 2^127 and a score a few bits above those before it, the others have none: weights are never
+    above 1, so that nothing passes the range on the way to a result inside it."""
+    n = 200000  # several steps for each warp: the token is the first of its warp's at few of the places
+    b = R.Batch([n], 1, 64, 64, seed=37)
+    q = torch.zeros(1, 4, 64)
+    q[..., 0] = 8.0
+    q = q.view(1, -1).to(torch.bfloat16)
+    b.k[0].zero_()
+    b.v[0].zero_()
+    with Cache(b, kv_type, cuda_device) as c:
+        for at in (70001, 100000, 100064, 100129, 100200, 100260, 199999):
+            for score in (0.5, 2.5):
+                b.k[0][at, 0, 0] = score
+                b.v[0][at] = torch.where(torch.arange(64) % 2 == 0, 2.0 ** 127, -1.5 * 2.0 ** 126).to(torch.bfloat16)
+                c.append()
+                out, lse = attend(c, q)
+                hold(b, kv_type, q, out)
+                b.k[0][at] = 0
+                b.v[0][at] = 0
+        assert c.error() == 0
