@@ -13,8 +13,6 @@ Variant variant_of(int type, int dim) {
                                 : attend_variant_int8(dim);
 }
 
-constexpr int kAttStatic = 3584;  // at least what the kernel's static shared memory takes
-
 // Warps and stages: the most warps that leave each 2 stages; their first pieces (state_bytes each) stay in shared memory where
 // that costs no warp.
 struct Geometry {

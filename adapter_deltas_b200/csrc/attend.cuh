@@ -292,6 +292,30 @@ __device__ __forceinline__ void store8(uint8_t *out, const float (&y)[8], float 
 struct Step {
   int seq, unit, pos, len;  // sequence, unit, first token of the step, tokens of the sequence
 };
+// At its range's end a warp's state takes the place of its ring, two stages at least.
+constexpr bool state_fits(int type, int dim, bool any, int tt, int rows) {
+  for (int d = any ? 16 : dim; d <= dim; d += 16)
+    if (state_floats(rows, d) * 4 > 2 * tt * kv_tile_bytes(type, d)) return false;
+  return true;
+}
+
+// What the warps of a block share beside their rings.
+struct AttendShared {
+  uint64_t full[kAttMaxWarps][kAttMaxStages];
+  Step held[kAttMaxWarps][kAttMaxStages];
+  // a warp's first slot, from its sequence's first, and that sequence and its length; last entry: the block's last slot
+  longlong2 scan[kAttMaxWarps];
+  long long from[kAttMaxWarps + 1];
+  int2 start[kAttMaxWarps + 1];
+  int4 piece[2 * kAttMaxWarps];  // [2 warp + which]: {sequence (-1: none), unit, cut before 1 / after 2, -}
+  const float *where[2 * kAttMaxWarps];
+  int order[2 * kAttMaxWarps], run[2 * kAttMaxWarps + 1];  // pieces in order; where each unit's run starts
+  int n_runs, dead_block;
+  int2 to_join[2];  // {first block, blocks} of units that this block was the last to work on
+};
+constexpr int kAttStatic = 3584;  // kept free of rings for it
+static_assert(sizeof(AttendShared) <= kAttStatic, "the shared memory beside the rings");
+
 // A unit as its key head and the first of its query heads in that head's group, in one number.
 __device__ __forceinline__ int pack_unit(int kvh, int h0) { return kvh << 16 | h0; }
 __device__ __forceinline__ int unit_kvh(int unit) { return unit >> 16; }
@@ -315,17 +339,19 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(KvView kv, KvSeqs
   const int tile_bytes = kv_tile_bytes(TYPE, dim), stage_bytes = TT * tile_bytes;
 
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ uint64_t full[kAttMaxWarps][kAttMaxStages];
-  __shared__ Step held[kAttMaxWarps][kAttMaxStages];
-  // a warp's first slot, from its sequence's first, and that sequence and its length; last entry: the block's last slot
-  __shared__ longlong2 scan[kAttMaxWarps];
-  __shared__ long long from[kAttMaxWarps + 1];
-  __shared__ int2 start[kAttMaxWarps + 1];
-  __shared__ int4 piece[2 * kAttMaxWarps];  // [2 warp + which]: {sequence (-1: none), unit, cut before 1 / after 2, -}
-  __shared__ const float *where[2 * kAttMaxWarps];
-  __shared__ int order[2 * kAttMaxWarps], run[2 * kAttMaxWarps + 1];  // pieces in order; where each unit's run starts
-  __shared__ int n_runs, dead_block;
-  __shared__ int2 to_join[2];  // {first block, blocks} of units that this block was the last to work on
+  __shared__ AttendShared sh;
+  auto &full = sh.full;
+  auto &held = sh.held;
+  auto &scan = sh.scan;
+  auto &from = sh.from;
+  auto &start = sh.start;
+  auto &piece = sh.piece;
+  auto &where = sh.where;
+  auto &order = sh.order;
+  auto &run = sh.run;
+  int &n_runs = sh.n_runs, &dead_block = sh.dead_block;
+  auto &to_join = sh.to_join;
+  static_assert(state_fits(TYPE, DIM, ANY, TT, ROWS), "a state has to fit into the smallest ring");
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int n_warps = blockDim.x >> 5;
