@@ -46,6 +46,8 @@
 // in their places (the end of a page, before the window) may be anything.
 #pragma once
 
+#include <cfloat>
+
 #include "kv.cuh"
 
 namespace lora {
@@ -214,12 +216,14 @@ struct Ends {
 };
 __device__ __forceinline__ Ends finish(const float *sinks, int head, float m, float l) {
   Ends e;
-  const float sink = sinks ? sinks[head] * 1.44269504f : -INFINITY;
+  const float given = sinks ? sinks[head] : -INFINITY;
+  // (in base 2 within the range too: one at its end is a number still)
+  const float sink = fabsf(given) < INFINITY ? fminf(fmaxf(given * 1.44269504f, -FLT_MAX), FLT_MAX) : given;
   float base = fmaxf(m, sink);
   base = base == -INFINITY ? 0.f : base;
   if (sinks) l = l * exp2_fast(m - base) + exp2_fast(sink - base);
   e.mul = l == 0.f ? 0.f : __fdividef(exp2_fast(m - base), l);  // (nothing has any weight: zeros, as without a token)
-  e.lse = (base + __log2f(l)) * 0.693147181f;
+  e.lse = fmaf(__log2f(l), 0.693147181f, sink > m ? given : base * 0.693147181f);
   return e;
 }
 
