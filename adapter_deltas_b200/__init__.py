@@ -445,9 +445,9 @@ def lora_kv_create(device: int, n_layers: int, n_pages: int, page_tokens: int, n
 
 
 def lora_kv_destroy(kv: KvHandle) -> None:
-    if kv.ptr:
-        _check(_lib.lora_kv_destroy(kv), "lora_kv_destroy")
-        kv.ptr = 0
+    ptr, kv.ptr = kv.ptr, 0  # (freed even where the call reports an error: not to be passed again)
+    if ptr:
+        _check(_lib.lora_kv_destroy(ptr), "lora_kv_destroy")
 
 
 def lora_kv_get_error(kv: KvHandle, stream=None) -> int:
