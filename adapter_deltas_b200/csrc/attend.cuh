@@ -11,7 +11,7 @@
 //
 // Bound by HBM: 4 flops per cached element and query head, at most 16 query
 // heads to a byte.  (64 requests of 200 to 4000 tokens, bf16, 32 heads of 128: 1.15 GB
-// in 182 us, 6.3 TB/s; 512 of 64 to 2048, e4m3, 32 / 8 heads: 585 MB in 110 us, 5.3 TB/s.
+// in 182 us, 6.3 TB/s; 512 of 64 to 2048, e4m3, 32 / 8 heads: 585 MB in 111 us, 5.3 TB/s.
 // Short calls are latency: 16 requests of up to 100 tokens 9 us.)  So the split is by bytes, evenly, whatever the lengths:
 //  - The batch is one flat list of slots, ordered by (sequence, unit, step).  A
 //    unit is one key head with up to 8 (or 16) of its query heads; a step is 16
@@ -42,6 +42,10 @@
 // fp16 exactly, in 2 to 5 instructions per four; K's scales multiply the
 // scores, V's the weights, in fp32.
 //
+// More than 16 query heads to a key head are several units, each of which reads
+// the key head's tiles again (128 requests of 2000 to 4000 tokens over one key head
+// of 128, bf16: 45 us for 16 heads, 61 for 32, 101 for 64).
+//
 // Tokens outside the range get weight 0 by selection, not by adding: what lies
 // in their places (the end of a page, before the window) may be anything.
 #pragma once
@@ -56,7 +60,7 @@ constexpr int kAttMaxWarps = 12;
 constexpr int kAttMaxStages = 8;
 constexpr int kAttSmem = 227 * 1024;
 constexpr int kSlack = 4, kWeight = 11;  // powers of two (kWeight + kSlack: within fp16)
-constexpr int kCutSteps = 3;
+constexpr int kCutSteps = 3;  // 3 to 12 choose alike in all that was measured
 constexpr int kMaxSlotsLog2 = 30;  // of a block: counted in 32 bits
 
 struct AttendArgs {
@@ -449,11 +453,11 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(KvView kv, KvSeqs
   const unsigned long long slots_all = (unsigned long long)(total & kSlotBits) * a.units;
   const bool too_long = slots_all > (unsigned long long)gridDim.x << kMaxSlotsLog2;
   const unsigned long long units_all = (unsigned long long)(total >> kCountAt) * a.units;
-  // A unit cut between blocks costs their last one about 3 steps' time, in each
+  // A unit cut between blocks costs their last one kCutSteps steps' time or so, in each
   // warp.  While blocks of whole units are longer by less than that, none is cut
-  // (attention alone, whole and cut: 16 requests of up to 100 tokens 10.1 and 15.3
-  // us, 256 requests with a window of 128 20.1 and 23.2; 64 requests of 200 to 4000
-  // tokens 319 and 187, which are cut).
+  // (attention alone, whole and cut: 16 requests of up to 100 tokens 9.2 and 12.4
+  // us, 256 requests with a window of 128 20.3 and 21.4; 64 requests of 200 to 4000
+  // tokens 317 and 181, 37 of 5 to 9001 with 16 heads of 256 143 and 50, which are cut).
   const unsigned long long most_units = quotient(units_all + gridDim.x - 1, gridDim.x);  // of a block
   const bool by_units = most_units * longest * gridDim.x <= slots_all + (unsigned long long)kCutSteps * n_warps * gridDim.x;
   // (two slots at least to a block, so that it has a step: the join counts on
@@ -1252,11 +1256,12 @@ using AttendKernel = void (*)(KvView, KvSeqs, AttendArgs);
 // Which kernel takes a cache and a number of heads:
 //  - a step has as many tiles as give it about 8 KiB, so that its own cost (a
 //    wait, the running maximum) is spread over as many bytes: one tile instead of
-//    two took 127 instead of 119 us for 512 requests of e4m3, 32 / 8 heads of 128;
+//    two took 121 instead of 111 us for 512 requests of e4m3, 32 / 8 heads of 128;
 //  - 12 warps where their registers suffice (up to 8 heads a unit, dims up to 128):
-//    64 requests of bf16, 32 heads of 128, 191 us, with 8 warps 196; 512 of e4m3 143
-//    and 163 us at the time; 8 where accumulators would spill: 64 / 4 heads of 128,
-//    e4m3, 100 us, with 12 warps 118;
+//    64 requests of bf16, 32 heads of 128, 182.5 us, with 8 warps 190; 512 of e4m3 111
+//    and 117; 8 where accumulators would spill: 512 of e4m3, 64 / 4 heads of 128, 95 us,
+//    with 12 warps 127.  (9 to 16 heads wider than 128 spill 50 to 260 bytes all the same:
+//    a warp's 16 x 256 sums and as many of q are more than its registers.)
 //  - the usual widths are constants, others take the loops of the next larger one
 //    with a test for each 16 dims.
 struct Variant {

@@ -13,12 +13,14 @@
 // shuffles.  An append's block takes `rows` consecutive rows of the batch, so
 // many that the blocks are resident at once: its start, a chain of dependent
 // reads, is paid once, beside its first loads (4096 rows of 32 heads of 128 as
-// e4m3: 25 us, 102 MB at 4.1 TB/s; with 1 row a block 29).  What bounds the 8-bit
-// append beside HBM is the instructions per element, so addresses are kept per
-// thread and stepped.  A gather's block takes what its threads hold in flight
+// e4m3: 25 us, 102 MB at 4.0 TB/s; int8 30; bf16 26.5, 134 MB at 5.1; with 1 row a
+// block e4m3 29).  The 8-bit append is bound by neither (issue slots 67 % in use, DRAM
+// 33 %): its loads, the maximum over a vector's threads and the quotients follow
+// one another.  Addresses are kept per thread and stepped.  A gather's block takes what its threads hold in flight
 // twice over: its accesses, 128 bytes of a head here and there, are then close in
 // time to the rest of their tiles (11734 rows of that cache: 50 us, 291 MB at
-// 5.8 TB/s; resident blocks of 16 rows 60, 1 row, which leaves threads idle, 63).
+// 5.8 TB/s, int8 51; bf16 64, 385 MB at 6.0; resident blocks of 16 rows 60, 1 row,
+// which leaves threads idle, 63).
 // The block's warps look up the rows' sequences (a 32-way search in
 // row_offsets, two dependent reads up to 1024 sequences, where the row before is
 // not in the same one), then a thread a row its length and page; append reads
@@ -126,7 +128,7 @@ __host__ __device__ constexpr int vec_elements(int type) { return 16 / kv_elt(ty
 
 // A thread's 16 values of a bf16 row are 32 bytes.  As one access they are a sector
 // of its own; in two halves every sector is touched twice (gather of 11734 rows of
-// 32 heads of 128, e4m3: 60 and 62 us before its blocks were cut to two turns).
+// 32 heads of 128, e4m3: 50 and 54 us).
 __device__ __forceinline__ void load32(const uint8_t *p, bool wide, uint4 &a, uint4 &b) {
   if (wide) {
     asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"

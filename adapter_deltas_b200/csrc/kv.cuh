@@ -116,7 +116,7 @@ __device__ __forceinline__ Quant quant_of(float amax) {
 }
 // x * qmax / amax, and the same for two values with the packed fp32 instructions,
 // half as many (append of 4096 rows, 32 heads of 128: 25.1 and 27.3 us; the
-// norm has no registers left for the pairs: 48.3 and 49.4 us for 8192 x 4096).
+// norm has no registers left for the pairs: 48.7 and 50.1 us for 8192 x 4096).
 __device__ __forceinline__ float quant_div(float x, const Quant &q) {
   const float a = x * q.mul, t = a * q.rcp;
   return fmaf(fmaf(-t, q.amax, a), q.rcp, t);

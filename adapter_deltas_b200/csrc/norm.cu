@@ -14,9 +14,12 @@
 // scale per row, once for the largest magnitude.  A group's lanes are
 // neighbours in a warp, so its scale needs no shared memory.  Four vectors a
 // thread where there are many rows: few threads then wait at a row's two meetings
-// and an SM has 100 KB on their way (8192 x 4096: 48 us, 96 % of a copy's rate;
-// two vectors 56 us, one 68 us); two where rows are fewer than four to an SM
-// and the time is one row's latency (one row 2.4 us; four vectors 2.7 us).
+// and an SM has 100 KB on their way (8192 x 4096 in the full form, passes of a graph:
+// 48.7 us, 95 % of a copy's rate, though a thread spills 24 bytes; two vectors
+// 54.7 us, one 70.4); two where rows are fewer than four to an SM and the time is
+// one row's latency (one row 2.3 us, 512 4.3; four vectors 2.7 and 4.7).  Rows of 33
+// to 128 vectors are blocks of one warp, 32 to an SM at most (16384 x 512 with y alone:
+// 18 us for 34 MB).
 #include "kv.cuh"
 
 namespace lora {

@@ -537,9 +537,10 @@ LORA_API int lora_apply_noalloc(lora_pool *pool, int target, const void *x, int 
 /*
  * Between the adapted projections of a decode step: keys and values of the
  * requests' tokens in pages of caller-owned device memory, located through a
- * page table -- the unified paging of "Multi-LoRA Serving: Sharing One GPU
- * Across Adapters" (section "How S-LoRA Proved the Model"), where cache pages
- * live beside adapter pages.  The caller owns the table and hands out pages.
+ * page table, as the unified paging of "Multi-LoRA Serving: Sharing One GPU
+ * Across Adapters" (section "How S-LoRA Proved the Model") locates both.  The
+ * caller owns the table and hands out pages.  A cache has memory of its own,
+ * apart from an adapter pool's.
  *
  * A cache is n_layers x n_pages pages of page_tokens tokens x n_kv_heads heads
  * x head_dim, held as kv_type: bf16 as it comes, or 8-bit codes with one fp32
@@ -600,8 +601,8 @@ LORA_API int lora_kv_get_error(lora_kv *kv, int *device_status, void *stream);
  *                sequence s (none, one or many).  NULL: T == n_seqs and row s is
  *                the last token of sequence s (decode).
  * One launch.  Rows outside every segment, and rows of a sequence of length
- * -1, are skipped.  The sticky LORA_ERR_BAD_ID is raised by a sequence whose
- * length is below -1, past max_pages or less than its rows (none of them is
+ * -1, are skipped.  The sticky LORA_ERR_BAD_ID is raised by a sequence with rows
+ * whose length is below -1, past max_pages or less than its rows (none of them is
  * written), by a token on a page outside [0, n_pages) (that token is not
  * written) and by offsets out of order (rows in doubt are skipped).  No two
  * sequences of a call may share the page of a token that it writes.
@@ -675,7 +676,7 @@ LORA_API int lora_attend(lora_kv *kv, int layer, const void *q, int ldq, void *o
  *   eps                >= 0
  *   y, ldy             device bf16 [T, ldy]: n, or NULL
  *   q, ldq             device e4m3 [T, ldq] (one byte each): the codes of n for a
- *                      base product in 8 bits, or NULL (y and q not both)
+ *                      base product in 8 bits, or NULL (but one of y and q)
  *   q_scales, group    device fp32: with group 0 [T], one scale per row; else
  *                      [T, d / group], one per `group` columns (16, 32, 64, 128
  *                      or 256, dividing d).  Quantised as the cache's e4m3 rows.
