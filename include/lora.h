@@ -612,7 +612,7 @@ LORA_API int lora_kv_append(lora_kv *kv, int layer, const void *k, int ldk, cons
                    int n_seqs, int T, void *stream);
 
 /*
- * Read held tokens back as bf16, the values rounded once: the converse of
+ * Read held tokens back as bf16 (the fp32 products code * scale, rounded): the converse of
  * lora_kv_append with the same arguments, k and v being written (rows that
  * are skipped or in error keep what they held).  k and v must not overlap;
  * they may be column slices of one buffer.  One launch.
