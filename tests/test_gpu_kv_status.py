@@ -48,6 +48,7 @@ def test_reading_waits_for_its_stream_alone(cuda_device, batch):
     side = torch.cuda.Stream()
     with Cache(batch, "bf16", cuda_device) as c:
         c.bad = torch.tensor([33, 20], dtype=torch.int32, device=cuda_device)
+        assert c.error() == L.LORA_OK  # (a kernel's first launch loads it, which may wait for the device)
         torch.cuda.synchronize()
         done = torch.cuda.Event()
         bad_append(c, side)
